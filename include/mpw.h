@@ -548,6 +548,91 @@ MPW_API mpw_status mpw_qlinear_fp8(const uint8_t* xq, const float* sx, const uin
                                    mpw_stream_t stream);
 
 /*
+ * Int8 linear for codes of 4..8 bits.
+ * Pages: DynaQuant "Custom kernel architecture" (packed codes expanded to a
+ * tensor-core format; 6- to 8-bit codes are not exact in E4M3 but are in
+ * int8).  The activations take the tutorial's symmetric per-channel formula
+ * per token, with max_int = 127:
+ *   sx_m = fl32(max_k |x_mk| / 127) (a zero token: fl32(1 / 127)),
+ *   xq_mk = clamp(rint_half_even(fl32(x_mk / sx_m)), -127, 127),
+ *   y_mn = bf16_rn(s_n * sx_m * sum_k xq_mk q_nk), the sum exact in int32.
+ * A token with an infinity or NaN gets sx = NaN and codes 0: its outputs (and
+ * every weight gradient it enters) are NaN, other tokens are unaffected.
+ * xq is stored as canonical 8-bit packed rows (row stride 16 * ceil(K / 16) =
+ * mpw_packed_row_bytes(K, 8), zero padding), so (xq, sx) is at once the
+ * operand of the product, an 8-bit checkpoint of x for the backward pass
+ * (mpw_qlinear_grad_w_int8), and something mpw_unpack and mpw_dequantize read.
+ *
+ * mpw_quantize_x_int8 -- x bf16 [M, K] -> xq rows and sx fp32 [M].
+ *   xq  device, uint8 [M, mpw_packed_row_bytes(K, 8)], 16-byte aligned.
+ *   Any M >= 1 and K >= 1; x needs only its natural alignment (16-byte
+ *   aligned rows, K % 8 == 0, are read fastest).
+ */
+MPW_API mpw_status mpw_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, uint8_t* xq, float* sx,
+                                       mpw_stream_t stream);
+
+/*
+ * mpw_qlinear_int8 -- y = sx * (xq @ q^T) * s in 8-bit integers.
+ *   xq, sx   from mpw_quantize_x_int8 (several linears may share them).
+ *   packed, scales  as produced by mpw_quantize_pack, bits 4..8 (else
+ *            MPW_E_UNSUPPORTED_BITS), in `layout` (MPW_LAYOUT_*; paired needs
+ *            K % 32 == 0).
+ *   y        device, bf16 [M, N].
+ *   workspace  device, 16-byte aligned, of mpw_qlinear_int8_workspace_bytes
+ *            (0: may be NULL); its contents need no preparation and mean
+ *            nothing after the call.  Calls that may run at the same time
+ *            need one each; it must live until the call has run (and, when
+ *            captured, as long as the graph).  Missing or too small:
+ *            MPW_E_INVALID_ARG.
+ *   Any M, N >= 1; 1 <= K <= 131071 (a 32-bit sum cannot overflow).
+ *   One token or 2048, the result is the same exact sum, scaled in fp32 and
+ *   rounded once.
+ */
+MPW_API size_t mpw_qlinear_int8_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K);
+MPW_API mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales,
+                                    int bits, int layout, int64_t M, int64_t N, int64_t K, uint16_t* y,
+                                    void* workspace, size_t workspace_bytes, mpw_stream_t stream);
+
+/*
+ * Gradients of a packed linear y = x @ (q * s)^T.
+ * Pages: DynaQuant "Step 1: sensitivity" (a per-matrix statistic of the
+ * weight gradient, which mpw_allocate_bits takes); tutorial, exercises
+ * (straight-through training of quantized layers).  Both are the gradients
+ * of the product with respect to its factors, the roundings passed straight
+ * through.
+ *
+ * mpw_qlinear_grad_x -- dx = dy @ (q * s).
+ *   dy       device, bf16 [M, N]; 16-byte aligned when N % 8 == 0 (else
+ *            MPW_E_MISALIGNED), otherwise natural alignment.
+ *   packed, scales, bits (4..15), layout  the linear's rows.
+ *   dx       device, bf16 [M, K]: bf16_rn(sum_n dy_mn bf16_rn(s_n q_nk)), the
+ *            sum in fp32 (the weight operand of the bf16 tensor cores is
+ *            rounded once, at most 2^-8 of its value).
+ *   workspace  as for mpw_qlinear_int8, of mpw_qlinear_grad_x_workspace_bytes.
+ *
+ * mpw_qlinear_grad_w_int8 -- dW = dy^T @ x, x read from its 8-bit checkpoint.
+ *   dy       as for mpw_qlinear_grad_x.
+ *   xq, sx   from mpw_quantize_x_int8 of the forward pass's x [M, K].
+ *   dW_type  MPW_GRAD_BF16: dW bf16 [N, K], the operand sx_m xq_mk rounded to
+ *            bf16, fp32 sums.  MPW_GRAD_F32: dW fp32 [N, K], the operand as a
+ *            sum of two bf16 values (2^-16 of its value), fp32 sums.
+ *   accumulate  nonzero (MPW_GRAD_F32 only, else MPW_E_INVALID_ARG): added to
+ *            dW instead of replacing it.
+ *   workspace  as above, of mpw_qlinear_grad_w_int8_workspace_bytes.
+ * Any M, N, K >= 1; results do not depend on what ran before (no atomics on
+ * floating-point values).
+ */
+typedef enum mpw_grad_type { MPW_GRAD_BF16 = 0, MPW_GRAD_F32 = 1 } mpw_grad_type;
+MPW_API size_t mpw_qlinear_grad_x_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K);
+MPW_API mpw_status mpw_qlinear_grad_x(const uint16_t* dy, const uint8_t* packed, const float* scales, int bits,
+                                      int layout, int64_t M, int64_t N, int64_t K, uint16_t* dx, void* workspace,
+                                      size_t workspace_bytes, mpw_stream_t stream);
+MPW_API size_t mpw_qlinear_grad_w_int8_workspace_bytes(int dW_type, int64_t M, int64_t N, int64_t K);
+MPW_API mpw_status mpw_qlinear_grad_w_int8(const uint16_t* dy, const uint8_t* xq, const float* sx, int64_t M,
+                                           int64_t N, int64_t K, void* dW, int dW_type, int accumulate,
+                                           void* workspace, size_t workspace_bytes, mpw_stream_t stream);
+
+/*
  * mpw_gather_shards -- re-orders the gathered outputs of an output-row
  * (N) sharded linear into y.  No page describes tensor parallelism; the
  * partition is this library's: rank r of `world` owns weight rows

@@ -21,6 +21,7 @@ __all__ = [
     "recipe_plan", "save_packed", "load_packed", "Pass", "pass_dependencies",
     "LAYOUTS", "workspace", "qlinear_workspace_bytes", "quantize_pack_groups", "qlinear_groups",
     "gather_shards", "quantize_x_fp8", "qlinear_fp8",
+    "quantize_x_int8", "qlinear_int8", "qlinear_grad_x", "qlinear_grad_w_int8",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmpw.so")
@@ -41,6 +42,9 @@ PATHS = {"auto": 0, "gemv": 1, "gemm": 2}
 # Packed layouts (mpw_layout): the canonical stream and its paired-halves
 # re-ordering, which the decode kernels read fastest (K % 32 == 0).
 LAYOUTS = {"canonical": 0, "paired": 1}
+# dW types of mpw_qlinear_grad_w_int8 (mpw_grad_type)
+GRAD_BF16 = 0
+GRAD_F32 = 1
 # mpw_qlinear_flags: x was written before the launch preceding the run of
 # flagged calls
 X_READY = 1
@@ -156,6 +160,20 @@ def _load():
     L.mpw_quantize_x_fp8.restype = c_int
     L.mpw_qlinear_fp8.argtypes = [vp, vp, vp, vp, c_int, c_int, i64, i64, i64, vp, vp]
     L.mpw_qlinear_fp8.restype = c_int
+    L.mpw_quantize_x_int8.argtypes = [vp, i64, i64, vp, vp, vp]
+    L.mpw_quantize_x_int8.restype = c_int
+    L.mpw_qlinear_int8_workspace_bytes.argtypes = [c_int, c_int, i64, i64, i64]
+    L.mpw_qlinear_int8_workspace_bytes.restype = ctypes.c_size_t
+    L.mpw_qlinear_int8.argtypes = [vp, vp, vp, vp, c_int, c_int, i64, i64, i64, vp, vp, ctypes.c_size_t, vp]
+    L.mpw_qlinear_int8.restype = c_int
+    L.mpw_qlinear_grad_x_workspace_bytes.argtypes = [c_int, c_int, i64, i64, i64]
+    L.mpw_qlinear_grad_x_workspace_bytes.restype = ctypes.c_size_t
+    L.mpw_qlinear_grad_x.argtypes = [vp, vp, vp, c_int, c_int, i64, i64, i64, vp, vp, ctypes.c_size_t, vp]
+    L.mpw_qlinear_grad_x.restype = c_int
+    L.mpw_qlinear_grad_w_int8_workspace_bytes.argtypes = [c_int, i64, i64, i64]
+    L.mpw_qlinear_grad_w_int8_workspace_bytes.restype = ctypes.c_size_t
+    L.mpw_qlinear_grad_w_int8.argtypes = [vp, vp, vp, i64, i64, i64, vp, c_int, c_int, vp, ctypes.c_size_t, vp]
+    L.mpw_qlinear_grad_w_int8.restype = c_int
     L.mpw_gather_shards.argtypes = [vp, i64, i64, i64, i64, vp, vp]
     L.mpw_gather_shards.restype = c_int
     L.mpw_device_error.argtypes = [ctypes.POINTER(i32)]
@@ -446,6 +464,184 @@ def qlinear_fp8(x, packed, scales, bits: int, y=None, layout: str = "canonical",
     _check(lib.mpw_qlinear_fp8(xq.data_ptr(), sx.data_ptr(), packed.data_ptr(), scales.data_ptr(), int(bits),
                                LAYOUTS[layout], M, N, K, y.data_ptr(), _stream(stream)), "mpw_qlinear_fp8")
     return y
+
+
+def _need_shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _need_here(**tensors):
+    """Every tensor on the current device (kernels run there)."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _scratch(nbytes: int, stream, workspace):
+    """The caller's workspace after a check, or a fresh one: taken from torch's
+    allocator on the stream the kernels run on, so that it is not handed out
+    again before they are done (and belongs to the graph when captured)."""
+    import torch
+
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace", 1)
+        _need_here(workspace=workspace)
+        if workspace.numel() < nbytes:
+            raise ValueError(f"workspace must hold {nbytes} bytes, got {workspace.numel()}")
+        return workspace
+    if nbytes == 0:
+        return None
+    dev = torch.device("cuda", torch.cuda.current_device())
+    handle = _stream(stream)
+    if handle == torch.cuda.current_stream().cuda_stream:
+        return torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
+        return torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel()
+
+
+def quantize_x_int8(x, xq=None, sx=None, stream=None):
+    """x bf16 [M, K] -> (xq uint8 [M, packed_row_bytes(K, 8)], sx fp32 [M]):
+    per-token 8-bit activations as canonical 8-bit packed rows
+    (mpw_quantize_x_int8); the operand of qlinear_int8 and the checkpoint
+    qlinear_grad_w_int8 reads."""
+    import torch
+
+    _need(x, torch.bfloat16, "x", 2)
+    M, K = x.shape
+    rb = packed_row_bytes(K, 8)
+    if xq is None:
+        xq = torch.empty((M, rb), dtype=torch.uint8, device=x.device)
+    if sx is None:
+        sx = torch.empty((M,), dtype=torch.float32, device=x.device)
+    _need(xq, torch.uint8, "xq", 2)
+    _need(sx, torch.float32, "sx", 1)
+    _need_shape(xq, (M, rb), "xq")
+    _need_shape(sx, (M,), "sx")
+    _need_here(x=x, xq=xq, sx=sx)
+    _check(lib.mpw_quantize_x_int8(x.data_ptr(), M, K, xq.data_ptr(), sx.data_ptr(), _stream(stream)),
+           "mpw_quantize_x_int8")
+    return xq, sx
+
+
+def _need_rows(packed, scales, bits: int, K: int):
+    import torch
+
+    _need(packed, torch.uint8, "packed", 2)
+    _need(scales, torch.float32, "scales", 1)
+    if packed.shape[1] != packed_row_bytes(K, bits):
+        raise ValueError("packed rows must be exactly packed_row_bytes(K, bits) long")
+    _need_shape(scales, (packed.shape[0],), "scales")
+
+
+def _need_codes(xq, sx, K: int):
+    import torch
+
+    _need(xq, torch.uint8, "xq", 2)
+    _need(sx, torch.float32, "sx", 1)
+    if xq.shape[1] != packed_row_bytes(K, 8):
+        raise ValueError("xq rows must be exactly packed_row_bytes(K, 8) long")
+    _need_shape(sx, (xq.shape[0],), "sx")
+
+
+def qlinear_int8(x, packed, scales, bits: int, y=None, layout: str = "canonical", xq=None, sx=None, K=None,
+                 workspace=None, stream=None):
+    """Int8 linear for codes of 4..8 bits (mpw_qlinear_int8): quantizes x per
+    token unless (xq, sx) are given (then x may be None and K names the number
+    of inputs), then y bf16 [M, N].  ``workspace``: uint8 of at least
+    lib.mpw_qlinear_int8_workspace_bytes; allocated per call when None."""
+    import torch
+
+    if (xq is None) != (sx is None):
+        raise ValueError("xq and sx go together")
+    if xq is None:
+        xq, sx = quantize_x_int8(x, stream=stream)
+        K = x.shape[1]
+    elif K is None:
+        if x is None:
+            raise ValueError("K is needed when only xq and sx are given")
+        K = x.shape[1]
+    K = int(K)
+    _need_codes(xq, sx, K)
+    _need_rows(packed, scales, bits, K)
+    M, N = xq.shape[0], packed.shape[0]
+    if y is None:
+        y = torch.empty((M, N), dtype=torch.bfloat16, device=packed.device)
+    _need(y, torch.bfloat16, "y", 2)
+    _need_shape(y, (M, N), "y")
+    _need_here(xq=xq, sx=sx, packed=packed, scales=scales, y=y)
+    ws = _scratch(int(lib.mpw_qlinear_int8_workspace_bytes(int(bits), LAYOUTS[layout], M, N, K)), stream, workspace)
+    _check(lib.mpw_qlinear_int8(xq.data_ptr(), sx.data_ptr(), packed.data_ptr(), scales.data_ptr(), int(bits),
+                                LAYOUTS[layout], M, N, K, y.data_ptr(), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "mpw_qlinear_int8")
+    return y
+
+
+def qlinear_grad_x(dy, packed, scales, bits: int, K: int, dx=None, layout: str = "canonical", workspace=None,
+                   stream=None):
+    """dx = dy @ (q * s): the gradient of a packed linear's input
+    (mpw_qlinear_grad_x); dy bf16 [M, N] -> dx bf16 [M, K], bits 4..15."""
+    import torch
+
+    K = int(K)
+    _need(dy, torch.bfloat16, "dy", 2)
+    _need_rows(packed, scales, bits, K)
+    M, N = dy.shape
+    if packed.shape[0] != N:
+        raise ValueError("packed must have one row per column of dy")
+    if dx is None:
+        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
+    _need(dx, torch.bfloat16, "dx", 2)
+    _need_shape(dx, (M, K), "dx")
+    _need_here(dy=dy, packed=packed, scales=scales, dx=dx)
+    ws = _scratch(int(lib.mpw_qlinear_grad_x_workspace_bytes(int(bits), LAYOUTS[layout], M, N, K)), stream, workspace)
+    _check(lib.mpw_qlinear_grad_x(dy.data_ptr(), packed.data_ptr(), scales.data_ptr(), int(bits), LAYOUTS[layout], M,
+                                  N, K, dx.data_ptr(), _ptr(ws), _nbytes(ws), _stream(stream)), "mpw_qlinear_grad_x")
+    return dx
+
+
+def qlinear_grad_w_int8(dy, xq, sx, K: int, dW=None, dtype=None, accumulate: bool = False, workspace=None,
+                        stream=None):
+    """dW = dy^T @ x with x read from its 8-bit checkpoint (xq, sx) of
+    quantize_x_int8 (mpw_qlinear_grad_w_int8): dy bf16 [M, N] -> dW [N, K] in
+    ``dtype`` (bfloat16, the default, or float32; that of ``dW`` when given).
+    ``accumulate`` adds to a given float32 dW."""
+    import torch
+
+    K = int(K)
+    _need(dy, torch.bfloat16, "dy", 2)
+    _need_codes(xq, sx, K)
+    M, N = dy.shape
+    if xq.shape[0] != M:
+        raise ValueError("dy and xq must have the same number of tokens")
+    if dtype is None:
+        dtype = torch.bfloat16 if dW is None else dW.dtype
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dW must be torch.bfloat16 or torch.float32")
+    if accumulate and (dW is None or dtype != torch.float32):
+        raise ValueError("accumulate needs a float32 dW")
+    if dW is None:
+        dW = torch.empty((N, K), dtype=dtype, device=dy.device)
+    _need(dW, dtype, "dW", 2)
+    _need_shape(dW, (N, K), "dW")
+    _need_here(dy=dy, xq=xq, sx=sx, dW=dW)
+    kind = GRAD_F32 if dtype == torch.float32 else GRAD_BF16
+    ws = _scratch(int(lib.mpw_qlinear_grad_w_int8_workspace_bytes(kind, M, N, K)), stream, workspace)
+    _check(lib.mpw_qlinear_grad_w_int8(dy.data_ptr(), xq.data_ptr(), sx.data_ptr(), M, N, K, dW.data_ptr(), kind,
+                                       int(bool(accumulate)), _ptr(ws), _nbytes(ws), _stream(stream)),
+           "mpw_qlinear_grad_w_int8")
+    return dW
 
 
 def gather_shards(blocks, world: int, M: int, Nl: int, N: int, y=None, stream=None):

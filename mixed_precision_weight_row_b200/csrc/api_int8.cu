@@ -1,0 +1,133 @@
+// C ABI of the int8 linear and of the gradients of packed linears: argument
+// validation, workspace layout and kernel dispatch.  See mpw.h for the
+// contract of every entry point.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "int8_internal.h"
+#include "mpw.h"
+#include "mpw_internal.h"
+
+using namespace mpw;
+
+namespace {
+
+constexpr int64_t kMaxDim = 0x3fffffff;   // rows, columns and tokens (tensor-map coordinates are 32-bit)
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+mpw_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MPW_OK : MPW_E_CUDA; }
+bool layout_ok(int layout) { return layout == MPW_LAYOUT_CANONICAL || layout == MPW_LAYOUT_PAIRED; }
+bool bits_ok(int bits, int most) { return bits >= kMinBits && bits <= most; }
+bool dims_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 1 && N >= 1 && K >= 1 && M <= kMaxDim && N <= kMaxDim && K <= kMaxDim;
+}
+size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+// Canonical 8-bit rows already are rows of signed bytes.
+bool rows_are_bytes(int bits, int layout) { return bits == 8 && layout == MPW_LAYOUT_CANONICAL; }
+
+size_t expanded_bf16_bytes(int64_t rows, int64_t cols) {
+  return round256(static_cast<size_t>(rows) * static_cast<size_t>(stride_bf16(cols)) * 2);
+}
+
+// TMA reads rows of whole 16 bytes: dy is copied to padded rows when N % 8 != 0.
+size_t padded_dy_bytes(int64_t M, int64_t N) { return N % 8 == 0 ? 0 : expanded_bf16_bytes(M, N); }
+bool dy_aligned(const uint16_t* dy, int64_t N) { return aligned(dy, N % 8 == 0 ? 16 : 2); }
+mpw_status padded_dy(const uint16_t** dy, int64_t M, int64_t N, uint8_t* room, cudaStream_t s) {
+  if (N % 8 == 0) return MPW_OK;
+  uint16_t* out = reinterpret_cast<uint16_t*>(room);
+  const mpw_status st = from_cuda(launch_pad_bf16(*dy, M, N, out, s));
+  *dy = out;
+  return st;
+}
+
+}  // namespace
+
+extern "C" {
+
+mpw_status mpw_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, uint8_t* xq, float* sx, mpw_stream_t stream) {
+  if (x == nullptr || xq == nullptr || sx == nullptr || !dims_ok(M, 1, K)) return MPW_E_INVALID_ARG;
+  if (!aligned(x, 2) || !aligned(xq, 16) || !aligned(sx, 4)) return MPW_E_MISALIGNED;
+  return from_cuda(launch_quantize_x_int8(x, M, K, xq, sx, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t mpw_qlinear_int8_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K) {
+  if (!bits_ok(bits, 8) || !layout_ok(layout) || !dims_ok(M, N, K) || K > kInt8MaxK) return 0;
+  if (rows_are_bytes(bits, layout)) return 0;
+  return round256(static_cast<size_t>(N) * static_cast<size_t>(stride_i8(K)));
+}
+
+mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int bits,
+                            int layout, int64_t M, int64_t N, int64_t K, uint16_t* y, void* workspace,
+                            size_t workspace_bytes, mpw_stream_t stream) {
+  if (!bits_ok(bits, 8)) return MPW_E_UNSUPPORTED_BITS;
+  if (xq == nullptr || sx == nullptr || packed == nullptr || scales == nullptr || y == nullptr) return MPW_E_INVALID_ARG;
+  if (!dims_ok(M, N, K) || K > kInt8MaxK || !layout_ok(layout)) return MPW_E_INVALID_ARG;
+  if (layout == MPW_LAYOUT_PAIRED && K % 32 != 0) return MPW_E_INVALID_ARG;
+  if (!aligned(xq, 16) || !aligned(packed, 16) || !aligned(sx, 4) || !aligned(scales, 4) || !aligned(y, 2))
+    return MPW_E_MISALIGNED;
+  const size_t need = mpw_qlinear_int8_workspace_bytes(bits, layout, M, N, K);
+  if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return MPW_E_INVALID_ARG;
+  if (need != 0 && !aligned(workspace, 16)) return MPW_E_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const uint8_t* w = packed;
+  if (!rows_are_bytes(bits, layout)) {
+    const cudaError_t e = launch_expand_i8(packed, N, K, bits, layout, static_cast<uint8_t*>(workspace), s);
+    if (e != cudaSuccess) return MPW_E_CUDA;
+    w = static_cast<const uint8_t*>(workspace);
+  }
+  return from_cuda(launch_dense_i8(xq, w, sx, scales, 8 - bits, M, N, K, y, s));
+}
+
+size_t mpw_qlinear_grad_x_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K) {
+  if (!bits_ok(bits, kMaxBits) || !layout_ok(layout) || !dims_ok(M, N, K)) return 0;
+  return expanded_bf16_bytes(N, K) + padded_dy_bytes(M, N);
+}
+
+mpw_status mpw_qlinear_grad_x(const uint16_t* dy, const uint8_t* packed, const float* scales, int bits, int layout,
+                              int64_t M, int64_t N, int64_t K, uint16_t* dx, void* workspace, size_t workspace_bytes,
+                              mpw_stream_t stream) {
+  if (!bits_ok(bits, kMaxBits)) return MPW_E_UNSUPPORTED_BITS;
+  if (dy == nullptr || packed == nullptr || scales == nullptr || dx == nullptr) return MPW_E_INVALID_ARG;
+  if (!dims_ok(M, N, K) || !layout_ok(layout)) return MPW_E_INVALID_ARG;
+  if (layout == MPW_LAYOUT_PAIRED && K % 32 != 0) return MPW_E_INVALID_ARG;
+  if (!dy_aligned(dy, N) || !aligned(packed, 16) || !aligned(scales, 4) || !aligned(dx, 2)) return MPW_E_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < mpw_qlinear_grad_x_workspace_bytes(bits, layout, M, N, K))
+    return MPW_E_INVALID_ARG;
+  if (!aligned(workspace, 16)) return MPW_E_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint16_t* w = reinterpret_cast<uint16_t*>(ws);
+  mpw_status st = from_cuda(launch_expand_bf16(packed, scales, N, K, bits, layout, w, s));
+  if (st == MPW_OK) st = padded_dy(&dy, M, N, ws + expanded_bf16_bytes(N, K), s);
+  if (st != MPW_OK) return st;
+  return from_cuda(launch_dense_grad_x(dy, w, M, N, K, dx, s));
+}
+
+size_t mpw_qlinear_grad_w_int8_workspace_bytes(int dW_type, int64_t M, int64_t N, int64_t K) {
+  if ((dW_type != MPW_GRAD_BF16 && dW_type != MPW_GRAD_F32) || !dims_ok(M, N, K)) return 0;
+  return expanded_bf16_bytes((dW_type == MPW_GRAD_F32 ? 2 : 1) * M, K) + padded_dy_bytes(M, N);
+}
+
+mpw_status mpw_qlinear_grad_w_int8(const uint16_t* dy, const uint8_t* xq, const float* sx, int64_t M, int64_t N,
+                                   int64_t K, void* dW, int dW_type, int accumulate, void* workspace,
+                                   size_t workspace_bytes, mpw_stream_t stream) {
+  if (dy == nullptr || xq == nullptr || sx == nullptr || dW == nullptr) return MPW_E_INVALID_ARG;
+  if (!dims_ok(M, N, K) || (dW_type != MPW_GRAD_BF16 && dW_type != MPW_GRAD_F32)) return MPW_E_INVALID_ARG;
+  const bool f32 = dW_type == MPW_GRAD_F32;
+  if (accumulate != 0 && !f32) return MPW_E_INVALID_ARG;
+  if (!dy_aligned(dy, N) || !aligned(xq, 16) || !aligned(sx, 4) || !aligned(dW, f32 ? 4 : 2)) return MPW_E_MISALIGNED;
+  if (workspace == nullptr || workspace_bytes < mpw_qlinear_grad_w_int8_workspace_bytes(dW_type, M, N, K))
+    return MPW_E_INVALID_ARG;
+  if (!aligned(workspace, 16)) return MPW_E_MISALIGNED;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int parts = f32 ? 2 : 1;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint16_t* x = reinterpret_cast<uint16_t*>(ws);
+  mpw_status st = from_cuda(launch_expand_x(xq, sx, M, K, parts, x, s));
+  if (st == MPW_OK) st = padded_dy(&dy, M, N, ws + expanded_bf16_bytes(parts * M, K), s);
+  if (st != MPW_OK) return st;
+  return from_cuda(launch_dense_grad_w(dy, x, parts, M, N, K, dW, f32, accumulate != 0, s));
+}
+
+}  // extern "C"

@@ -1,0 +1,45 @@
+// Internal declarations of the int8 linear and of the gradients of packed
+// linears.  As in mpw_internal.h, the C-ABI layer has checked every argument.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace mpw {
+
+// Largest K of an int8 product: 128 * 127 * K < 2^31.
+constexpr int64_t kInt8MaxK = 131071;
+
+// Row strides of the operands the dense GEMM reads by TMA: whole 16 bytes.
+inline int64_t stride_i8(int64_t K) { return (K + 15) / 16 * 16; }   // bytes
+inline int64_t stride_bf16(int64_t K) { return (K + 7) / 8 * 8; }    // elements
+
+// int8_ops.cu
+cudaError_t launch_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, uint8_t* xq, float* sx,
+                                   cudaStream_t stream);
+// Packed rows (4..8 bits) -> left-justified bytes, rows of stride_i8(K).
+cudaError_t launch_expand_i8(const uint8_t* packed, int64_t N, int64_t K, int bits, int layout, uint8_t* out,
+                             cudaStream_t stream);
+// Packed rows (4..15 bits) -> bf16_rn(s_n * q), rows of stride_bf16(K).
+cudaError_t launch_expand_bf16(const uint8_t* packed, const float* scales, int64_t N, int64_t K, int bits,
+                               int layout, uint16_t* out, cudaStream_t stream);
+// 8-bit activations -> bf16 rows of stride_bf16(K): hi = bf16_rn(sx * xq), and,
+// with parts == 2, in the M rows behind, bf16_rn(sx * xq - hi).
+cudaError_t launch_expand_x(const uint8_t* xq, const float* sx, int64_t M, int64_t K, int parts, uint16_t* out,
+                            cudaStream_t stream);
+// bf16 [rows, cols] -> the same with rows of stride_bf16(cols).
+cudaError_t launch_pad_bf16(const uint16_t* in, int64_t rows, int64_t cols, uint16_t* out, cudaStream_t stream);
+
+// gemm_dense.cu: products of operands laid out for TMA (rows of a stride that
+// is a multiple of 16 bytes, 16-byte aligned).
+//   y[m, n] = bf16(s_n * sx_m * (sum_k a[m, k] b[n, k]) / 2^shift), a and b signed bytes
+cudaError_t launch_dense_i8(const uint8_t* a, const uint8_t* b, const float* sx, const float* scales, int shift,
+                            int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream);
+//   dx[m, k] = bf16(sum_n dy[m, n] w[n, k])
+cudaError_t launch_dense_grad_x(const uint16_t* dy, const uint16_t* w, int64_t M, int64_t N, int64_t K, uint16_t* dx,
+                                cudaStream_t stream);
+//   dw[n, k] (+)= sum_m dy[m, n] (x[m, k] [+ x[M + m, k] with parts == 2])
+cudaError_t launch_dense_grad_w(const uint16_t* dy, const uint16_t* x, int parts, int64_t M, int64_t N, int64_t K,
+                                void* dw, bool f32, bool accumulate, cudaStream_t stream);
+
+}  // namespace mpw

@@ -34,6 +34,13 @@ from .quant import (  # noqa: F401
     unpack_paired,
     unpadded_row_bytes,
 )
+from .int8 import (  # noqa: F401
+    grad_w_ref,
+    grad_x_ref,
+    pack_rows_int8,
+    qlinear_int8_ref,
+    quantize_x_int8,
+)
 from .fp8 import (  # noqa: F401
     E4M3_MAX,
     FP8_MAX_BITS,
