@@ -206,11 +206,23 @@ def _check(status: int, where: str) -> None:
         raise MPWError(status, where)
 
 
-def _stream(stream=None) -> int:
-    import torch
+_torch_module = None
 
+
+def _torch():
+    """torch, imported on first use (the host-only entry points do without)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+
+        _torch_module = torch
+    return _torch_module
+
+
+def _stream(stream=None) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -466,49 +478,74 @@ def qlinear_fp8(x, packed, scales, bits: int, y=None, layout: str = "canonical",
     return y
 
 
-def _need_shape(t, shape, name):
-    if tuple(t.shape) != tuple(shape):
+def _arg(t, name: str, dtype, dev: int, shape=None, ndim: int = 0):
+    """One tensor argument: a contiguous CUDA tensor of this dtype on the
+    current device (kernels run there), of this shape or number of dims."""
+    if type(t) is not _torch().Tensor and not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if shape is None:
+        if t.dim() != ndim:
+            raise ValueError(f"{name} must have {ndim} dims")
+    elif t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _need_here(**tensors):
-    """Every tensor on the current device (kernels run there)."""
-    import torch
+def _here(t, name: str) -> int:
+    """The current device, once the call's first argument is known to be a
+    CUDA tensor (asking for it starts CUDA)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch._C._cuda_getDevice()
 
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t.device.index != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
-
-def _scratch(nbytes: int, stream, workspace):
-    """The caller's workspace after a check, or a fresh one: taken from torch's
-    allocator on the stream the kernels run on, so that it is not handed out
-    again before they are done (and belongs to the graph when captured)."""
-    import torch
-
+def _scratch(nbytes: int, handle: int, dev: int, workspace):
+    """(address, bytes, owner) of the caller's workspace after a check, or of a
+    fresh one: taken from torch's allocator on the stream the kernels run on,
+    so that it is not handed out again before they are done (and belongs to
+    the graph when captured)."""
+    torch = _torch()
     if workspace is not None:
-        _need(workspace, torch.uint8, "workspace", 1)
-        _need_here(workspace=workspace)
+        _arg(workspace, "workspace", torch.uint8, dev, ndim=1)
         if workspace.numel() < nbytes:
             raise ValueError(f"workspace must hold {nbytes} bytes, got {workspace.numel()}")
-        return workspace
+        return workspace.data_ptr(), workspace.numel(), workspace
     if nbytes == 0:
-        return None
-    dev = torch.device("cuda", torch.cuda.current_device())
-    handle = _stream(stream)
-    if handle == torch.cuda.current_stream().cuda_stream:
-        return torch.empty((nbytes,), dtype=torch.uint8, device=dev)
-    with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-        return torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        return None, 0, None
+    if handle == torch._C._cuda_getCurrentRawStream(dev):
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device="cuda")
+    else:
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
+            ws = torch.empty((nbytes,), dtype=torch.uint8, device="cuda")
+    return ws.data_ptr(), nbytes, ws
 
 
-def _ptr(t):
-    return None if t is None else t.data_ptr()
+def _row_bytes8(K: int) -> int:
+    return (K + 15) // 16 * 16
 
 
-def _nbytes(t) -> int:
-    return 0 if t is None else t.numel()
+def _rows_arg(packed, scales, bits: int, N, K: int, dev: int):
+    """Packed rows of K codes and their scales; returns the number of rows."""
+    torch = _torch()
+    rb = packed_row_bytes(K, bits)
+    if rb == 0 and not 4 <= bits <= 15:
+        raise MPWError(MPW_E_UNSUPPORTED_BITS, "packed rows")
+    if N is None:
+        _arg(packed, "packed", torch.uint8, dev, ndim=2)
+        N = packed.shape[0]
+    _arg(packed, "packed", torch.uint8, dev, shape=(N, rb))
+    _arg(scales, "scales", torch.float32, dev, shape=(N,))
+    return N
 
 
 def quantize_x_int8(x, xq=None, sx=None, stream=None):
@@ -516,43 +553,24 @@ def quantize_x_int8(x, xq=None, sx=None, stream=None):
     per-token 8-bit activations as canonical 8-bit packed rows
     (mpw_quantize_x_int8); the operand of qlinear_int8 and the checkpoint
     qlinear_grad_w_int8 reads."""
-    import torch
-
-    _need(x, torch.bfloat16, "x", 2)
+    torch = _torch()
+    if getattr(x, "dtype", None) != torch.bfloat16:
+        raise TypeError("x must be a torch.bfloat16 tensor")
+    dev = _here(x, "x")
+    _arg(x, "x", torch.bfloat16, dev, ndim=2)
     M, K = x.shape
-    rb = packed_row_bytes(K, 8)
+    rb = _row_bytes8(K)
     if xq is None:
-        xq = torch.empty((M, rb), dtype=torch.uint8, device=x.device)
+        xq = x.new_empty((M, rb), dtype=torch.uint8)
+    else:
+        _arg(xq, "xq", torch.uint8, dev, shape=(M, rb))
     if sx is None:
-        sx = torch.empty((M,), dtype=torch.float32, device=x.device)
-    _need(xq, torch.uint8, "xq", 2)
-    _need(sx, torch.float32, "sx", 1)
-    _need_shape(xq, (M, rb), "xq")
-    _need_shape(sx, (M,), "sx")
-    _need_here(x=x, xq=xq, sx=sx)
+        sx = x.new_empty((M,), dtype=torch.float32)
+    else:
+        _arg(sx, "sx", torch.float32, dev, shape=(M,))
     _check(lib.mpw_quantize_x_int8(x.data_ptr(), M, K, xq.data_ptr(), sx.data_ptr(), _stream(stream)),
            "mpw_quantize_x_int8")
     return xq, sx
-
-
-def _need_rows(packed, scales, bits: int, K: int):
-    import torch
-
-    _need(packed, torch.uint8, "packed", 2)
-    _need(scales, torch.float32, "scales", 1)
-    if packed.shape[1] != packed_row_bytes(K, bits):
-        raise ValueError("packed rows must be exactly packed_row_bytes(K, bits) long")
-    _need_shape(scales, (packed.shape[0],), "scales")
-
-
-def _need_codes(xq, sx, K: int):
-    import torch
-
-    _need(xq, torch.uint8, "xq", 2)
-    _need(sx, torch.float32, "sx", 1)
-    if xq.shape[1] != packed_row_bytes(K, 8):
-        raise ValueError("xq rows must be exactly packed_row_bytes(K, 8) long")
-    _need_shape(sx, (xq.shape[0],), "sx")
 
 
 def qlinear_int8(x, packed, scales, bits: int, y=None, layout: str = "canonical", xq=None, sx=None, K=None,
@@ -560,31 +578,35 @@ def qlinear_int8(x, packed, scales, bits: int, y=None, layout: str = "canonical"
     """Int8 linear for codes of 4..8 bits (mpw_qlinear_int8): quantizes x per
     token unless (xq, sx) are given (then x may be None and K names the number
     of inputs), then y bf16 [M, N].  ``workspace``: uint8 of at least
-    lib.mpw_qlinear_int8_workspace_bytes; allocated per call when None."""
-    import torch
-
+    qlinear_int8_workspace_bytes; allocated per call when None."""
+    torch = _torch()
+    dev = _here(packed, "packed")
+    bits = int(bits)
     if (xq is None) != (sx is None):
         raise ValueError("xq and sx go together")
     if xq is None:
         xq, sx = quantize_x_int8(x, stream=stream)
-        K = x.shape[1]
-    elif K is None:
-        if x is None:
-            raise ValueError("K is needed when only xq and sx are given")
-        K = x.shape[1]
-    K = int(K)
-    _need_codes(xq, sx, K)
-    _need_rows(packed, scales, bits, K)
-    M, N = xq.shape[0], packed.shape[0]
+        M, K = x.shape
+    else:
+        if K is None:
+            if x is None:
+                raise ValueError("K is needed when only xq and sx are given")
+            K = x.shape[1]
+        K = int(K)
+        _arg(xq, "xq", torch.uint8, dev, ndim=2)
+        M = xq.shape[0]
+        _arg(xq, "xq", torch.uint8, dev, shape=(M, _row_bytes8(K)))
+        _arg(sx, "sx", torch.float32, dev, shape=(M,))
+    N = _rows_arg(packed, scales, bits, None, K, dev)
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=packed.device)
-    _need(y, torch.bfloat16, "y", 2)
-    _need_shape(y, (M, N), "y")
-    _need_here(xq=xq, sx=sx, packed=packed, scales=scales, y=y)
-    ws = _scratch(int(lib.mpw_qlinear_int8_workspace_bytes(int(bits), LAYOUTS[layout], M, N, K)), stream, workspace)
-    _check(lib.mpw_qlinear_int8(xq.data_ptr(), sx.data_ptr(), packed.data_ptr(), scales.data_ptr(), int(bits),
-                                LAYOUTS[layout], M, N, K, y.data_ptr(), _ptr(ws), _nbytes(ws), _stream(stream)),
-           "mpw_qlinear_int8")
+        y = packed.new_empty((M, N), dtype=torch.bfloat16)
+    else:
+        _arg(y, "y", torch.bfloat16, dev, shape=(M, N))
+    lay = LAYOUTS[layout]
+    handle = _stream(stream)
+    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_int8_workspace_bytes(bits, lay, M, N, K), handle, dev, workspace)
+    _check(lib.mpw_qlinear_int8(xq.data_ptr(), sx.data_ptr(), packed.data_ptr(), scales.data_ptr(), bits, lay, M, N, K,
+                                y.data_ptr(), ws, ws_bytes, handle), "mpw_qlinear_int8")
     return y
 
 
@@ -592,22 +614,21 @@ def qlinear_grad_x(dy, packed, scales, bits: int, K: int, dx=None, layout: str =
                    stream=None):
     """dx = dy @ (q * s): the gradient of a packed linear's input
     (mpw_qlinear_grad_x); dy bf16 [M, N] -> dx bf16 [M, K], bits 4..15."""
-    import torch
-
-    K = int(K)
-    _need(dy, torch.bfloat16, "dy", 2)
-    _need_rows(packed, scales, bits, K)
+    torch = _torch()
+    dev = _here(dy, "dy")
+    bits, K = int(bits), int(K)
+    _arg(dy, "dy", torch.bfloat16, dev, ndim=2)
     M, N = dy.shape
-    if packed.shape[0] != N:
-        raise ValueError("packed must have one row per column of dy")
+    _rows_arg(packed, scales, bits, N, K, dev)
     if dx is None:
-        dx = torch.empty((M, K), dtype=torch.bfloat16, device=dy.device)
-    _need(dx, torch.bfloat16, "dx", 2)
-    _need_shape(dx, (M, K), "dx")
-    _need_here(dy=dy, packed=packed, scales=scales, dx=dx)
-    ws = _scratch(int(lib.mpw_qlinear_grad_x_workspace_bytes(int(bits), LAYOUTS[layout], M, N, K)), stream, workspace)
-    _check(lib.mpw_qlinear_grad_x(dy.data_ptr(), packed.data_ptr(), scales.data_ptr(), int(bits), LAYOUTS[layout], M,
-                                  N, K, dx.data_ptr(), _ptr(ws), _nbytes(ws), _stream(stream)), "mpw_qlinear_grad_x")
+        dx = dy.new_empty((M, K))
+    else:
+        _arg(dx, "dx", torch.bfloat16, dev, shape=(M, K))
+    lay = LAYOUTS[layout]
+    handle = _stream(stream)
+    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_grad_x_workspace_bytes(bits, lay, M, N, K), handle, dev, workspace)
+    _check(lib.mpw_qlinear_grad_x(dy.data_ptr(), packed.data_ptr(), scales.data_ptr(), bits, lay, M, N, K,
+                                  dx.data_ptr(), ws, ws_bytes, handle), "mpw_qlinear_grad_x")
     return dx
 
 
@@ -617,30 +638,28 @@ def qlinear_grad_w_int8(dy, xq, sx, K: int, dW=None, dtype=None, accumulate: boo
     quantize_x_int8 (mpw_qlinear_grad_w_int8): dy bf16 [M, N] -> dW [N, K] in
     ``dtype`` (bfloat16, the default, or float32; that of ``dW`` when given).
     ``accumulate`` adds to a given float32 dW."""
-    import torch
-
+    torch = _torch()
+    dev = _here(dy, "dy")
     K = int(K)
-    _need(dy, torch.bfloat16, "dy", 2)
-    _need_codes(xq, sx, K)
+    _arg(dy, "dy", torch.bfloat16, dev, ndim=2)
     M, N = dy.shape
-    if xq.shape[0] != M:
-        raise ValueError("dy and xq must have the same number of tokens")
+    _arg(xq, "xq", torch.uint8, dev, shape=(M, _row_bytes8(K)))
+    _arg(sx, "sx", torch.float32, dev, shape=(M,))
     if dtype is None:
         dtype = torch.bfloat16 if dW is None else dW.dtype
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype != torch.bfloat16 and dtype != torch.float32:
         raise TypeError("dW must be torch.bfloat16 or torch.float32")
     if accumulate and (dW is None or dtype != torch.float32):
         raise ValueError("accumulate needs a float32 dW")
     if dW is None:
-        dW = torch.empty((N, K), dtype=dtype, device=dy.device)
-    _need(dW, dtype, "dW", 2)
-    _need_shape(dW, (N, K), "dW")
-    _need_here(dy=dy, xq=xq, sx=sx, dW=dW)
+        dW = dy.new_empty((N, K), dtype=dtype)
+    else:
+        _arg(dW, "dW", dtype, dev, shape=(N, K))
     kind = GRAD_F32 if dtype == torch.float32 else GRAD_BF16
-    ws = _scratch(int(lib.mpw_qlinear_grad_w_int8_workspace_bytes(kind, M, N, K)), stream, workspace)
+    handle = _stream(stream)
+    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_grad_w_int8_workspace_bytes(kind, M, N, K), handle, dev, workspace)
     _check(lib.mpw_qlinear_grad_w_int8(dy.data_ptr(), xq.data_ptr(), sx.data_ptr(), M, N, K, dW.data_ptr(), kind,
-                                       int(bool(accumulate)), _ptr(ws), _nbytes(ws), _stream(stream)),
-           "mpw_qlinear_grad_w_int8")
+                                       int(bool(accumulate)), ws, ws_bytes, handle), "mpw_qlinear_grad_w_int8")
     return dW
 
 

@@ -26,6 +26,11 @@ size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 // Canonical 8-bit rows already are rows of signed bytes.
 bool rows_are_bytes(int bits, int layout) { return bits == 8 && layout == MPW_LAYOUT_CANONICAL; }
 
+// A few tokens take the kernel that streams packed rows (no workspace).
+bool few_tokens(int bits, int64_t M, int64_t K) {
+  return M <= 8 && gemv_i8_fits(M, K, static_cast<int64_t>(mpw_packed_row_bytes(K, bits)));
+}
+
 size_t expanded_bf16_bytes(int64_t rows, int64_t cols) {
   return round256(static_cast<size_t>(rows) * static_cast<size_t>(stride_bf16(cols)) * 2);
 }
@@ -53,7 +58,7 @@ mpw_status mpw_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, uint8_t*
 
 size_t mpw_qlinear_int8_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K) {
   if (!bits_ok(bits, 8) || !layout_ok(layout) || !dims_ok(M, N, K) || K > kInt8MaxK) return 0;
-  if (rows_are_bytes(bits, layout)) return 0;
+  if (rows_are_bytes(bits, layout) || few_tokens(bits, M, K)) return 0;
   return round256(static_cast<size_t>(N) * static_cast<size_t>(stride_i8(K)));
 }
 
@@ -70,6 +75,7 @@ mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* p
   if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return MPW_E_INVALID_ARG;
   if (need != 0 && !aligned(workspace, 16)) return MPW_E_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (few_tokens(bits, M, K)) return from_cuda(launch_gemv_i8(xq, sx, packed, scales, bits, layout, M, N, K, y, s));
   const uint8_t* w = packed;
   if (!rows_are_bytes(bits, layout)) {
     const cudaError_t e = launch_expand_i8(packed, N, K, bits, layout, static_cast<uint8_t*>(workspace), s);

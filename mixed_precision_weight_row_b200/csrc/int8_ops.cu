@@ -16,6 +16,7 @@
 #include "int8_expand.cuh"
 #include "int8_internal.h"
 #include "mpw_internal.h"
+#include "tc_ptx.cuh"
 
 namespace mpw {
 namespace {
@@ -42,11 +43,14 @@ __device__ __forceinline__ uint32_t code8(float x, float s) {
 // and a value above 0x7F80 (bf16 infinity) means a NaN was seen.
 __device__ __forceinline__ uint32_t mag2(uint32_t v) { return v & 0x7FFF7FFFu; }
 
-// One CTA per token.  Two passes over the row, the second from L1 / L2.
+// One CTA per token.  Two passes over the row, the second from L1 / L2.  The
+// next launch may start at once (the decode kernel reads weights before it waits
+// for this one).
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads)
 quantize_x_int8_kernel(const uint16_t* __restrict__ x, int K, int stride, uint8_t* __restrict__ xq,
                        float* __restrict__ sx) {
+  ptx::grid_dep_wait_then_release();
   __shared__ uint32_t red[kThreads / 32];
   const size_t m = blockIdx.x;
   const uint16_t* row = x + m * static_cast<size_t>(K);
