@@ -28,7 +28,7 @@ bool rows_are_bytes(int bits, int layout) { return bits == 8 && layout == MPW_LA
 
 // A few tokens take the kernel that streams packed rows (no workspace).
 bool few_tokens(int bits, int64_t M, int64_t K) {
-  return M <= 8 && gemv_i8_fits(M, K, static_cast<int64_t>(mpw_packed_row_bytes(K, bits)));
+  return gemv_i8_fits(bits, M, K);
 }
 
 size_t expanded_bf16_bytes(int64_t rows, int64_t cols) {

@@ -86,5 +86,109 @@ __device__ __forceinline__ void group(const uint32_t (&w)[B + 1], uint32_t (&o)[
   group_all<B, PAIRED>(w, o, std::make_integer_sequence<int, 8>{});
 }
 
+// ---------------------------------------------------------------------------
+// The same bytes in an order of k that takes fewer operations, for kernels
+// that can order x to match.  Codes repeat against byte borders every
+// U = 8 / gcd(8, B) codes (a unit of U * B / 8 bytes): byte p of four units
+// side by side in one word (a "plane") lets one shift and one mask place the
+// same code of all four, or two of each and an OR when it crosses a byte.
+// A plane takes one byte permute of paired words, whose halves hold two
+// streams already, and two or three of canonical ones; 4-bit codes need none and
+// 8-bit codes are left as they are.
+// ---------------------------------------------------------------------------
+
+template <int B>
+struct Unit {
+  static constexpr int codes = B == 8 ? 1 : (B == 4 ? 2 : (B == 6 ? 4 : 8));
+  static constexpr int bytes = codes * B / 8;
+};
+
+// Index in the group of the code in byte j of ordered word c.
+template <int B, bool PAIRED>
+__host__ __device__ constexpr int ordered_code(int c, int j) {
+  constexpr int U = Unit<B>::codes;
+  if (!PAIRED) {
+    const int block = c / U, in = c % U;             // four units in a row make a block of U words
+    return 4 * U * block + U * j + in;
+  }
+  // bytes 0, 1: two units of the even stream, bytes 2, 3: of the odd one
+  const int block = c / U, in = c % U;
+  return 2 * (2 * U * block + U * (j & 1) + in) + (j >> 1);
+}
+
+// Plane P of block K: byte P of its four units.
+template <int B, bool PAIRED, int K, int P>
+__device__ __forceinline__ uint32_t plane(const uint32_t (&w)[B + 1]) {
+  constexpr int S = Unit<B>::bytes;
+  if constexpr (PAIRED) {
+    constexpr int a = 2 * S * K + P, b = a + S;      // stream bytes of the two units
+    constexpr uint32_t sel = (a & 1) | (((b & 1) + 4) << 4) | (((a & 1) + 2) << 8) | (((b & 1) + 6) << 12);
+    return __byte_perm(w[a >> 1], w[b >> 1], sel);
+  } else {
+    constexpr int a = 4 * S * K + P, b = a + S, c = b + S, d = c + S;
+    constexpr uint32_t s1 = (a & 3) | (((b & 3) + 4) << 4), s2 = (c & 3) | (((d & 3) + 4) << 4);
+    return __byte_perm(__byte_perm(w[a >> 2], w[b >> 2], s1), __byte_perm(w[c >> 2], w[d >> 2], s2), 0x5410);
+  }
+}
+
+// Code C of the units whose planes are given, at the top of each byte.
+template <int B, int C, int S>
+__device__ __forceinline__ uint32_t from_planes(const uint32_t (&pl)[S]) {
+  constexpr int p = C * B >> 3, r = C * B & 7;
+  if constexpr (r + B <= 8) {
+    return shift<8 - B - r>(pl[p]) & Just<B>::kMask;
+  } else {
+    constexpr int low = 8 - r, high = B - low;       // bits in byte p and in byte p + 1
+    constexpr uint32_t ml = (((1u << low) - 1u) << (8 - B)) * 0x01010101u;
+    constexpr uint32_t mh = ((0xFFu << (8 - high)) & 0xFFu) * 0x01010101u;
+    return (shift<8 - B - r>(pl[p]) & ml) | (shift<8 - high>(pl[p + 1]) & mh);
+  }
+}
+
+template <int B, bool PAIRED, int K, int... P>
+__device__ __forceinline__ void block_planes(const uint32_t (&w)[B + 1], uint32_t (&pl)[Unit<B>::bytes],
+                                             std::integer_sequence<int, P...>) {
+  ((pl[P] = plane<B, PAIRED, K, P>(w)), ...);
+}
+
+template <int B, int K, int... C>
+__device__ __forceinline__ void block_codes(const uint32_t (&pl)[Unit<B>::bytes], uint32_t (&o)[8],
+                                            std::integer_sequence<int, C...>) {
+  ((o[K * Unit<B>::codes + C] = from_planes<B, C>(pl)), ...);
+}
+
+template <int B, bool PAIRED, int... K>
+__device__ __forceinline__ void ordered_all(const uint32_t (&w)[B + 1], uint32_t (&o)[8],
+                                            std::integer_sequence<int, K...>) {
+  (([&] {
+     uint32_t pl[Unit<B>::bytes];
+     block_planes<B, PAIRED, K>(w, pl, std::make_integer_sequence<int, Unit<B>::bytes>{});
+     block_codes<B, K>(pl, o, std::make_integer_sequence<int, Unit<B>::codes>{});
+   }()),
+   ...);
+}
+
+// One 32-code group -> 32 left-justified bytes, byte j of word c being code
+// ordered_code<B, PAIRED>(c, j).
+template <int B, bool PAIRED>
+__device__ __forceinline__ void group_ordered(const uint32_t (&w)[B + 1], uint32_t (&o)[8]) {
+  ordered_all<B, PAIRED>(w, o, std::make_integer_sequence<int, 8 / Unit<B>::codes>{});
+}
+
+// The bytes of x of one group (v in k order) in that order.
+template <int B, bool PAIRED>
+__device__ __forceinline__ void order_x(const uint32_t (&v)[8], uint32_t (&o)[8]) {
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int k = ordered_code<B, PAIRED>(c, j);
+      r |= ((v[k >> 2] >> (8 * (k & 3))) & 0xFFu) << (8 * j);
+    }
+    o[c] = r;
+  }
+}
+
 }  // namespace i8
 }  // namespace mpw

@@ -31,8 +31,8 @@ cudaError_t launch_expand_x(const uint8_t* xq, const float* sx, int64_t M, int64
 cudaError_t launch_pad_bf16(const uint16_t* in, int64_t rows, int64_t cols, uint16_t* out, cudaStream_t stream);
 
 // gemv_int8.cu: the int8 linear for up to 8 tokens, packed rows streamed once;
-// for shapes whose x and at least four rows fit in shared memory.
-bool gemv_i8_fits(int64_t M, int64_t K, int64_t slot_bytes);
+// for shapes whose x and the slots of eight warps fit in shared memory.
+bool gemv_i8_fits(int bits, int64_t M, int64_t K);
 cudaError_t launch_gemv_i8(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int bits,
                            int layout, int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream);
 
