@@ -26,9 +26,20 @@ size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 // Canonical 8-bit rows already are rows of signed bytes.
 bool rows_are_bytes(int bits, int layout) { return bits == 8 && layout == MPW_LAYOUT_CANONICAL; }
 
-// A few tokens take the kernel that streams packed rows (no workspace).
-bool few_tokens(int bits, int64_t M, int64_t K) {
-  return gemv_i8_fits(bits, M, K);
+// How a call of the int8 linear runs: a few tokens on the kernel that streams
+// packed rows, up to a thousand on the one that expands them on the way to the
+// tensor cores, more on expanded rows (the only one that takes a workspace).
+// One B200, us: 5120 x 6144, b = 6: 4 tokens 9.6 / 10.7 (first / second), 8
+// tokens 15.6 / 10.9; 5120 x 17408, b = 5: 2 tokens 14.7 / 22.6, 4 tokens 26.8
+// / 22.9; 17408 x 5120, b = 8: 4 tokens 20.1 / 17.5.  17408 x 5120, b = 6: 512
+// tokens 45 / 67 (second / third), 1024 tokens 86 / 88, 2048 tokens 168 / 141.
+// Rows that already are bytes need no expansion: 5120 x 6144, b = 8: 256
+// tokens 15.7 / 17.2, 512 tokens 22.2 / 19.0.
+enum class Int8Path { kGemv, kFused, kDense };
+Int8Path int8_path(int bits, int layout, int64_t M, int64_t N, int64_t K) {
+  if ((M <= 2 || (M <= 4 && K <= 8192 && bits <= 7)) && gemv_i8_fits(bits, M, K)) return Int8Path::kGemv;
+  if (M <= (rows_are_bytes(bits, layout) ? 256 : 1024) && gemm_i8_fits(M, N)) return Int8Path::kFused;
+  return Int8Path::kDense;
 }
 
 size_t expanded_bf16_bytes(int64_t rows, int64_t cols) {
@@ -58,7 +69,7 @@ mpw_status mpw_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, uint8_t*
 
 size_t mpw_qlinear_int8_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K) {
   if (!bits_ok(bits, 8) || !layout_ok(layout) || !dims_ok(M, N, K) || K > kInt8MaxK) return 0;
-  if (rows_are_bytes(bits, layout) || few_tokens(bits, M, K)) return 0;
+  if (rows_are_bytes(bits, layout) || int8_path(bits, layout, M, N, K) != Int8Path::kDense) return 0;
   return round256(static_cast<size_t>(N) * static_cast<size_t>(stride_i8(K)));
 }
 
@@ -75,7 +86,11 @@ mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* p
   if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return MPW_E_INVALID_ARG;
   if (need != 0 && !aligned(workspace, 16)) return MPW_E_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (few_tokens(bits, M, K)) return from_cuda(launch_gemv_i8(xq, sx, packed, scales, bits, layout, M, N, K, y, s));
+  switch (int8_path(bits, layout, M, N, K)) {
+    case Int8Path::kGemv: return from_cuda(launch_gemv_i8(xq, sx, packed, scales, bits, layout, M, N, K, y, s));
+    case Int8Path::kFused: return from_cuda(launch_gemm_i8(xq, sx, packed, scales, bits, layout, M, N, K, y, s));
+    case Int8Path::kDense: break;
+  }
   const uint8_t* w = packed;
   if (!rows_are_bytes(bits, layout)) {
     const cudaError_t e = launch_expand_i8(packed, N, K, bits, layout, static_cast<uint8_t*>(workspace), s);

@@ -249,8 +249,7 @@ cudaError_t run_m(const Args& p, cudaStream_t stream) {
   const bool two = p.N >= 16 * static_cast<int64_t>(device_info().num_sms);
   if (p.M == 1) return two ? run<B, PAIRED, 1, 2>(p, stream) : run<B, PAIRED, 1, 1>(p, stream);
   if (p.M == 2) return two ? run<B, PAIRED, 2, 2>(p, stream) : run<B, PAIRED, 2, 1>(p, stream);
-  if (p.M <= 4) return two ? run<B, PAIRED, 4, 2>(p, stream) : run<B, PAIRED, 4, 1>(p, stream);
-  return two ? run<B, PAIRED, 8, 2>(p, stream) : run<B, PAIRED, 8, 1>(p, stream);
+  return two ? run<B, PAIRED, 4, 2>(p, stream) : run<B, PAIRED, 4, 1>(p, stream);
 }
 
 template <int B>
@@ -261,8 +260,8 @@ cudaError_t run_layout(const Args& p, bool paired, cudaStream_t stream) {
 }  // namespace
 
 bool gemv_i8_fits(int bits, int64_t M, int64_t K) {
-  if (M > 8 || K > kInt8MaxK) return false;
-  const int mt = M <= 1 ? 1 : (M <= 2 ? 2 : (M <= 4 ? 4 : 8));
+  if (M > 4 || K > kInt8MaxK) return false;
+  const int mt = M <= 2 ? static_cast<int>(M) : 4;
   int n, codes;
   segments_of(static_cast<int>(K), &n, &codes);
   return x_bytes(mt, static_cast<int>(K)) + kTail + 8u * 2u * static_cast<uint32_t>(codes / 8 * bits) <= kSmemMax;

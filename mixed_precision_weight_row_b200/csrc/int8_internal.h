@@ -30,10 +30,16 @@ cudaError_t launch_expand_x(const uint8_t* xq, const float* sx, int64_t M, int64
 // bf16 [rows, cols] -> the same with rows of stride_bf16(cols).
 cudaError_t launch_pad_bf16(const uint16_t* in, int64_t rows, int64_t cols, uint16_t* out, cudaStream_t stream);
 
-// gemv_int8.cu: the int8 linear for up to 8 tokens, packed rows streamed once;
+// gemv_int8.cu: the int8 linear for up to 4 tokens, packed rows streamed once;
 // for shapes whose x and the slots of eight warps fit in shared memory.
 bool gemv_i8_fits(int bits, int64_t M, int64_t K);
 cudaError_t launch_gemv_i8(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int bits,
+                           int layout, int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream);
+
+// gemm_int8.cu: the int8 linear with packed rows expanded on the way to the
+// tensor cores, in tiles of up to 256 tokens.
+bool gemm_i8_fits(int64_t M, int64_t N);
+cudaError_t launch_gemm_i8(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int bits,
                            int layout, int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream);
 
 // gemm_dense.cu: products of operands laid out for TMA (rows of a stride that

@@ -175,13 +175,20 @@ def test_qlinear_int8_every_token_count(mpw, M):
     _check_linear(mpw, 520, 1280, M, 6, "canonical")
 
 
-@pytest.mark.parametrize("M", [1, 7, 40, 300, 700])
+@pytest.mark.parametrize("layout", ["canonical", "paired"])
+@pytest.mark.parametrize("b", [4, 5, 6, 7, 8])
+@pytest.mark.parametrize("N,K,M", [(40, 96, 1025), (257, 1024, 1111), (600, 160, 1500)])
+def test_qlinear_int8_many_tokens(mpw, N, K, M, b, layout):
+    _check_linear(mpw, N, K, M, b, layout)
+
+
+@pytest.mark.parametrize("M", [1, 7, 40, 300, 700, 1100])
 @pytest.mark.parametrize("b", [4, 7, 8])
 def test_qlinear_int8_long_rows(mpw, M, b):
     _check_linear(mpw, 72, 17408, M, b, "canonical")
 
 
-@pytest.mark.parametrize("M", [1, 20, 600])
+@pytest.mark.parametrize("M", [1, 20, 600, 1030])
 def test_qlinear_int8_largest_sums(mpw, M):
     """Every product +-127 * 127 over the longest K: the 32-bit sums hold."""
     torch = _torch()
@@ -376,7 +383,7 @@ def _all_ops(mpw, x, dy, packed, scales, b, K):
     return y, dx, dW
 
 
-@pytest.mark.parametrize("M", [1, 24, 300, 600])
+@pytest.mark.parametrize("M", [1, 24, 300, 1100])
 def test_captured_graphs_replay_with_new_inputs(mpw, M):
     """Two graphs captured one after another, replayed in turn: neither
     touches the other's scratch."""
@@ -409,9 +416,10 @@ def test_captured_graphs_replay_with_new_inputs(mpw, M):
     assert mpw.device_error() == 0
 
 
-def test_two_streams_at_once(mpw):
+@pytest.mark.parametrize("M", [2, 40, 300, 1100])
+def test_two_streams_at_once(mpw, M):
     torch = _torch()
-    M, N, K, b = 300, 1000, 1024, 6
+    N, K, b = 1000, 1024, 6
     packed, scales = _rows(mpw, _w(N, K, 1), b, "canonical")
     xs = [_x(M, K, i).cuda() for i in range(2)]
     dys = [_dy(M, N, i).cuda() for i in range(2)]
@@ -432,7 +440,7 @@ def test_two_streams_at_once(mpw):
 
 def test_stream_argument_and_callers_workspace(mpw):
     torch = _torch()
-    M, N, K, b = 200, 264, 512, 7
+    M, N, K, b = 1050, 264, 512, 7
     packed, scales = _rows(mpw, _w(N, K, 1), b, "canonical")
     x, dy = _x(M, K, 0).cuda(), _dy(M, N, 0).cuda()
     y0, dx0, dW0 = _all_ops(mpw, x, dy, packed, scales, b, K)
