@@ -191,7 +191,9 @@ class _Lib:
     def __getattr__(self, name):
         if _Lib._handle is None:
             _Lib._handle = _load()
-        return getattr(_Lib._handle, name)
+        fn = getattr(_Lib._handle, name)
+        self.__dict__[name] = fn          # found directly from now on
+        return fn
 
 
 lib = _Lib()
@@ -219,10 +221,10 @@ def _torch():
     return _torch_module
 
 
-def _stream(stream=None) -> int:
+def _stream(stream=None, dev=None) -> int:
     if stream is None:
         torch = _torch()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -478,10 +480,11 @@ def qlinear_fp8(x, packed, scales, bits: int, y=None, layout: str = "canonical",
     return y
 
 
-def _arg(t, name: str, dtype, dev: int, shape=None, ndim: int = 0):
-    """One tensor argument: a contiguous CUDA tensor of this dtype on the
-    current device (kernels run there), of this shape or number of dims."""
-    if type(t) is not _torch().Tensor and not isinstance(t, _torch().Tensor):
+def _arg(t, name: str, dtype, dev: int, shape) -> int:
+    """One tensor argument: contiguous, on the current CUDA device (kernels run
+    there), of this dtype and shape, where None stands for any size; returns
+    the first size."""
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -489,13 +492,16 @@ def _arg(t, name: str, dtype, dev: int, shape=None, ndim: int = 0):
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    if shape is None:
-        if t.dim() != ndim:
-            raise ValueError(f"{name} must have {ndim} dims")
-    elif t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    got = t.shape
+    if got != shape:
+        if len(got) != len(shape):
+            raise ValueError(f"{name} must have {len(shape)} dims")
+        for g, w in zip(got, shape):
+            if w is not None and g != w:
+                raise ValueError(f"{name} must have shape {shape}, got {tuple(got)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return got[0]
 
 
 def _here(t, name: str) -> int:
@@ -516,7 +522,7 @@ def _scratch(nbytes: int, handle: int, dev: int, workspace):
     the graph when captured)."""
     torch = _torch()
     if workspace is not None:
-        _arg(workspace, "workspace", torch.uint8, dev, ndim=1)
+        _arg(workspace, "workspace", torch.uint8, dev, (None,))
         if workspace.numel() < nbytes:
             raise ValueError(f"workspace must hold {nbytes} bytes, got {workspace.numel()}")
         return workspace.data_ptr(), workspace.numel(), workspace
@@ -534,17 +540,13 @@ def _row_bytes8(K: int) -> int:
     return (K + 15) // 16 * 16
 
 
-def _rows_arg(packed, scales, bits: int, N, K: int, dev: int):
+def _rows_arg(packed, scales, bits: int, N, K: int, dev: int) -> int:
     """Packed rows of K codes and their scales; returns the number of rows."""
     torch = _torch()
-    rb = packed_row_bytes(K, bits)
-    if rb == 0 and not 4 <= bits <= 15:
+    if not 4 <= bits <= 15:
         raise MPWError(MPW_E_UNSUPPORTED_BITS, "packed rows")
-    if N is None:
-        _arg(packed, "packed", torch.uint8, dev, ndim=2)
-        N = packed.shape[0]
-    _arg(packed, "packed", torch.uint8, dev, shape=(N, rb))
-    _arg(scales, "scales", torch.float32, dev, shape=(N,))
+    N = _arg(packed, "packed", torch.uint8, dev, (N, (K * bits + 127) // 128 * 16))
+    _arg(scales, "scales", torch.float32, dev, (N,))
     return N
 
 
@@ -557,18 +559,19 @@ def quantize_x_int8(x, xq=None, sx=None, stream=None):
     if getattr(x, "dtype", None) != torch.bfloat16:
         raise TypeError("x must be a torch.bfloat16 tensor")
     dev = _here(x, "x")
-    _arg(x, "x", torch.bfloat16, dev, ndim=2)
+    _arg(x, "x", torch.bfloat16, dev, (None, None))
     M, K = x.shape
     rb = _row_bytes8(K)
     if xq is None:
         xq = x.new_empty((M, rb), dtype=torch.uint8)
     else:
-        _arg(xq, "xq", torch.uint8, dev, shape=(M, rb))
+        _arg(xq, "xq", torch.uint8, dev, (M, rb))
     if sx is None:
         sx = x.new_empty((M,), dtype=torch.float32)
     else:
-        _arg(sx, "sx", torch.float32, dev, shape=(M,))
-    _check(lib.mpw_quantize_x_int8(x.data_ptr(), M, K, xq.data_ptr(), sx.data_ptr(), _stream(stream)),
+        _arg(sx, "sx", torch.float32, dev, (M,))
+    _check(lib.mpw_quantize_x_int8(x.data_ptr(), M, K, xq.data_ptr(), sx.data_ptr(),
+                                 _stream(stream, dev)),
            "mpw_quantize_x_int8")
     return xq, sx
 
@@ -593,17 +596,15 @@ def qlinear_int8(x, packed, scales, bits: int, y=None, layout: str = "canonical"
                 raise ValueError("K is needed when only xq and sx are given")
             K = x.shape[1]
         K = int(K)
-        _arg(xq, "xq", torch.uint8, dev, ndim=2)
-        M = xq.shape[0]
-        _arg(xq, "xq", torch.uint8, dev, shape=(M, _row_bytes8(K)))
-        _arg(sx, "sx", torch.float32, dev, shape=(M,))
+        M = _arg(xq, "xq", torch.uint8, dev, (None, _row_bytes8(K)))
+        _arg(sx, "sx", torch.float32, dev, (M,))
     N = _rows_arg(packed, scales, bits, None, K, dev)
     if y is None:
         y = packed.new_empty((M, N), dtype=torch.bfloat16)
     else:
-        _arg(y, "y", torch.bfloat16, dev, shape=(M, N))
+        _arg(y, "y", torch.bfloat16, dev, (M, N))
     lay = LAYOUTS[layout]
-    handle = _stream(stream)
+    handle = _stream(stream, dev)
     ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_int8_workspace_bytes(bits, lay, M, N, K), handle, dev, workspace)
     _check(lib.mpw_qlinear_int8(xq.data_ptr(), sx.data_ptr(), packed.data_ptr(), scales.data_ptr(), bits, lay, M, N, K,
                                 y.data_ptr(), ws, ws_bytes, handle), "mpw_qlinear_int8")
@@ -617,15 +618,15 @@ def qlinear_grad_x(dy, packed, scales, bits: int, K: int, dx=None, layout: str =
     torch = _torch()
     dev = _here(dy, "dy")
     bits, K = int(bits), int(K)
-    _arg(dy, "dy", torch.bfloat16, dev, ndim=2)
+    _arg(dy, "dy", torch.bfloat16, dev, (None, None))
     M, N = dy.shape
     _rows_arg(packed, scales, bits, N, K, dev)
     if dx is None:
         dx = dy.new_empty((M, K))
     else:
-        _arg(dx, "dx", torch.bfloat16, dev, shape=(M, K))
+        _arg(dx, "dx", torch.bfloat16, dev, (M, K))
     lay = LAYOUTS[layout]
-    handle = _stream(stream)
+    handle = _stream(stream, dev)
     ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_grad_x_workspace_bytes(bits, lay, M, N, K), handle, dev, workspace)
     _check(lib.mpw_qlinear_grad_x(dy.data_ptr(), packed.data_ptr(), scales.data_ptr(), bits, lay, M, N, K,
                                   dx.data_ptr(), ws, ws_bytes, handle), "mpw_qlinear_grad_x")
@@ -641,10 +642,10 @@ def qlinear_grad_w_int8(dy, xq, sx, K: int, dW=None, dtype=None, accumulate: boo
     torch = _torch()
     dev = _here(dy, "dy")
     K = int(K)
-    _arg(dy, "dy", torch.bfloat16, dev, ndim=2)
+    _arg(dy, "dy", torch.bfloat16, dev, (None, None))
     M, N = dy.shape
-    _arg(xq, "xq", torch.uint8, dev, shape=(M, _row_bytes8(K)))
-    _arg(sx, "sx", torch.float32, dev, shape=(M,))
+    _arg(xq, "xq", torch.uint8, dev, (M, _row_bytes8(K)))
+    _arg(sx, "sx", torch.float32, dev, (M,))
     if dtype is None:
         dtype = torch.bfloat16 if dW is None else dW.dtype
     if dtype != torch.bfloat16 and dtype != torch.float32:
@@ -654,9 +655,9 @@ def qlinear_grad_w_int8(dy, xq, sx, K: int, dW=None, dtype=None, accumulate: boo
     if dW is None:
         dW = dy.new_empty((N, K), dtype=dtype)
     else:
-        _arg(dW, "dW", dtype, dev, shape=(N, K))
+        _arg(dW, "dW", dtype, dev, (N, K))
     kind = GRAD_F32 if dtype == torch.float32 else GRAD_BF16
-    handle = _stream(stream)
+    handle = _stream(stream, dev)
     ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_grad_w_int8_workspace_bytes(kind, M, N, K), handle, dev, workspace)
     _check(lib.mpw_qlinear_grad_w_int8(dy.data_ptr(), xq.data_ptr(), sx.data_ptr(), M, N, K, dW.data_ptr(), kind,
                                        int(bool(accumulate)), ws, ws_bytes, handle), "mpw_qlinear_grad_w_int8")

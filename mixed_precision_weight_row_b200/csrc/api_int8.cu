@@ -42,6 +42,11 @@ Int8Path int8_path(int bits, int layout, int64_t M, int64_t N, int64_t K) {
   return Int8Path::kDense;
 }
 
+// Room for the expanded rows of the int8 linear.
+size_t int8_rows_bytes(int bits, int layout, int64_t N, int64_t K) {
+  return rows_are_bytes(bits, layout) ? 0 : round256(static_cast<size_t>(N) * static_cast<size_t>(stride_i8(K)));
+}
+
 size_t expanded_bf16_bytes(int64_t rows, int64_t cols) {
   return round256(static_cast<size_t>(rows) * static_cast<size_t>(stride_bf16(cols)) * 2);
 }
@@ -69,8 +74,7 @@ mpw_status mpw_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, uint8_t*
 
 size_t mpw_qlinear_int8_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K) {
   if (!bits_ok(bits, 8) || !layout_ok(layout) || !dims_ok(M, N, K) || K > kInt8MaxK) return 0;
-  if (rows_are_bytes(bits, layout) || int8_path(bits, layout, M, N, K) != Int8Path::kDense) return 0;
-  return round256(static_cast<size_t>(N) * static_cast<size_t>(stride_i8(K)));
+  return int8_path(bits, layout, M, N, K) == Int8Path::kDense ? int8_rows_bytes(bits, layout, N, K) : 0;
 }
 
 mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int bits,
@@ -91,18 +95,17 @@ mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* p
     case Int8Path::kFused: return from_cuda(launch_gemm_i8(xq, sx, packed, scales, bits, layout, M, N, K, y, s));
     case Int8Path::kDense: break;
   }
-  const uint8_t* w = packed;
-  if (!rows_are_bytes(bits, layout)) {
-    const cudaError_t e = launch_expand_i8(packed, N, K, bits, layout, static_cast<uint8_t*>(workspace), s);
+  uint8_t* rows = static_cast<uint8_t*>(workspace);
+  if (need != 0) {
+    const cudaError_t e = launch_expand_i8(packed, N, K, bits, layout, rows, s);
     if (e != cudaSuccess) return MPW_E_CUDA;
-    w = static_cast<const uint8_t*>(workspace);
   }
-  return from_cuda(launch_dense_i8(xq, w, sx, scales, 8 - bits, M, N, K, y, s));
+  return from_cuda(launch_dense_i8(xq, need != 0 ? rows : packed, sx, scales, 8 - bits, M, N, K, y, s));
 }
 
 size_t mpw_qlinear_grad_x_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K) {
   if (!bits_ok(bits, kMaxBits) || !layout_ok(layout) || !dims_ok(M, N, K)) return 0;
-  return expanded_bf16_bytes(N, K) + padded_dy_bytes(M, N);
+  return expanded_bf16_bytes(N, K) + padded_dy_bytes(M, N) + dense_workspace_bytes(M, K, dense_stages(N));
 }
 
 mpw_status mpw_qlinear_grad_x(const uint16_t* dy, const uint8_t* packed, const float* scales, int bits, int layout,
@@ -113,21 +116,24 @@ mpw_status mpw_qlinear_grad_x(const uint16_t* dy, const uint8_t* packed, const f
   if (!dims_ok(M, N, K) || !layout_ok(layout)) return MPW_E_INVALID_ARG;
   if (layout == MPW_LAYOUT_PAIRED && K % 32 != 0) return MPW_E_INVALID_ARG;
   if (!dy_aligned(dy, N) || !aligned(packed, 16) || !aligned(scales, 4) || !aligned(dx, 2)) return MPW_E_MISALIGNED;
-  if (workspace == nullptr || workspace_bytes < mpw_qlinear_grad_x_workspace_bytes(bits, layout, M, N, K))
-    return MPW_E_INVALID_ARG;
+  const size_t need = mpw_qlinear_grad_x_workspace_bytes(bits, layout, M, N, K);
+  if (workspace == nullptr || workspace_bytes < need) return MPW_E_INVALID_ARG;
   if (!aligned(workspace, 16)) return MPW_E_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* w = reinterpret_cast<uint16_t*>(ws);
+  uint8_t* room = ws + expanded_bf16_bytes(N, K);
   mpw_status st = from_cuda(launch_expand_bf16(packed, scales, N, K, bits, layout, w, s));
-  if (st == MPW_OK) st = padded_dy(&dy, M, N, ws + expanded_bf16_bytes(N, K), s);
+  if (st == MPW_OK) st = padded_dy(&dy, M, N, room, s);
   if (st != MPW_OK) return st;
-  return from_cuda(launch_dense_grad_x(dy, w, M, N, K, dx, s));
+  return from_cuda(launch_dense_grad_x(dy, w, M, N, K, dx, room + padded_dy_bytes(M, N), s));
 }
 
 size_t mpw_qlinear_grad_w_int8_workspace_bytes(int dW_type, int64_t M, int64_t N, int64_t K) {
   if ((dW_type != MPW_GRAD_BF16 && dW_type != MPW_GRAD_F32) || !dims_ok(M, N, K)) return 0;
-  return expanded_bf16_bytes((dW_type == MPW_GRAD_F32 ? 2 : 1) * M, K) + padded_dy_bytes(M, N);
+  const int parts = dW_type == MPW_GRAD_F32 ? 2 : 1;
+  return expanded_bf16_bytes(parts * M, K) + padded_dy_bytes(M, N) +
+         dense_workspace_bytes(N, K, parts * dense_stages(M));
 }
 
 mpw_status mpw_qlinear_grad_w_int8(const uint16_t* dy, const uint8_t* xq, const float* sx, int64_t M, int64_t N,
@@ -138,17 +144,19 @@ mpw_status mpw_qlinear_grad_w_int8(const uint16_t* dy, const uint8_t* xq, const 
   const bool f32 = dW_type == MPW_GRAD_F32;
   if (accumulate != 0 && !f32) return MPW_E_INVALID_ARG;
   if (!dy_aligned(dy, N) || !aligned(xq, 16) || !aligned(sx, 4) || !aligned(dW, f32 ? 4 : 2)) return MPW_E_MISALIGNED;
-  if (workspace == nullptr || workspace_bytes < mpw_qlinear_grad_w_int8_workspace_bytes(dW_type, M, N, K))
-    return MPW_E_INVALID_ARG;
+  const size_t need = mpw_qlinear_grad_w_int8_workspace_bytes(dW_type, M, N, K);
+  if (workspace == nullptr || workspace_bytes < need) return MPW_E_INVALID_ARG;
   if (!aligned(workspace, 16)) return MPW_E_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int parts = f32 ? 2 : 1;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* x = reinterpret_cast<uint16_t*>(ws);
+  uint8_t* room = ws + expanded_bf16_bytes(parts * M, K);
   mpw_status st = from_cuda(launch_expand_x(xq, sx, M, K, parts, x, s));
-  if (st == MPW_OK) st = padded_dy(&dy, M, N, ws + expanded_bf16_bytes(parts * M, K), s);
+  if (st == MPW_OK) st = padded_dy(&dy, M, N, room, s);
   if (st != MPW_OK) return st;
-  return from_cuda(launch_dense_grad_w(dy, x, parts, M, N, K, dW, f32, accumulate != 0, s));
+  return from_cuda(launch_dense_grad_w(dy, x, parts, M, N, K, dW, f32, accumulate != 0, room + padded_dy_bytes(M, N),
+                                       s));
 }
 
 }  // extern "C"

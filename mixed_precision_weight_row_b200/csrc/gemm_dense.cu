@@ -17,6 +17,12 @@
 // both into one of two accumulators in tensor memory, and four warps of each
 // write the other one out meanwhile.  Tiles run in groups of kGroup along i,
 // so that the CTAs working at one time share operand rows in L2.
+//
+// Tiles that do not fill a last round of the SM pairs are cut into slices of r
+// for all of them: a slice leaves its sums in a workspace, and a second kernel
+// adds the slices of a tile in their order and writes it.  (Letting the slice
+// that arrives last do so cost 40 us where this takes 5: one CTA pair reads what
+// here the whole GPU reads.)
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -24,15 +30,16 @@
 #include <stdint.h>
 
 #include "int8_internal.h"
+#include "lane_units.cuh"
 #include "mpw_internal.h"
 #include "tc_ptx.cuh"
 
 namespace mpw {
 namespace {
 
-constexpr int BM = 128;
-constexpr int kThreads = 256;
-constexpr int kEpiWarp0 = 4;
+constexpr int BM = 128;                  // rows of a tile per CTA of a pair
+constexpr int kThreads = 384;
+constexpr int kEpiWarp0 = 4;            // eight epilogue warps: two per 32 rows
 constexpr int kGroup = 8;                // tiles of 256 rows along i that share rows of b
 constexpr uint32_t kTmemCols = 512;      // two accumulators of up to 256 columns
 constexpr uint32_t kABytes = BM * 128;   // one stage of a
@@ -53,23 +60,20 @@ struct OpTraits {
 
 template <int BN>
 struct Tile {
-  static constexpr int rows_b = BN / 2;                  // rows of b per CTA
-  static constexpr int chunks_b = (rows_b + 63) / 64;    // 64-wide chunks of an MN-major b
-  template <bool MN>
-  static constexpr uint32_t b_bytes() { return MN ? chunks_b * 8192u : rows_b * 128u; }
-  template <bool MN>
-  static constexpr uint32_t stage() { return kABytes + b_bytes<MN>(); }
-  static constexpr uint32_t budget = 232448 - 1024 /*align*/ - 256 /*barriers*/;
-  template <bool MN>
-  static constexpr int stages() { return static_cast<int>(budget / stage<MN>()); }
-  template <bool MN>
-  static constexpr size_t smem() { return stages<MN>() * stage<MN>() + 1024 + 256; }
+  static constexpr uint32_t kStage = kABytes + BN / 2 * 128;     // half of the pair's rows of b
+  static constexpr int S = static_cast<int>((232448 - 1024 /*align*/ - 256 /*barriers*/) / kStage);
+  static constexpr size_t kSmem = S * kStage + 1024 + 256;
 };
+constexpr int kSlicedBN = 256;                                   // the width of tiles that may be sliced
+constexpr uint32_t kPartialWords = BM * kSlicedBN;               // sums of one CTA's half of a tile
 
 struct Args {
   int64_t I, J;          // results
   int blocks;            // stages along r per part
-  int parts;             // passes over r, part p reading slice p of b
+  int parts;             // passes over r, part p reading part p of b
+  int64_t whole;         // tiles done in one piece; those behind them in slices
+  int slices;
+  uint32_t* partial;     // sums of slices: [tile - whole][slice][256 rows x BN]
   void* out;             // [I, J]
   const float* row_scale;
   const float* col_scale;
@@ -77,28 +81,6 @@ struct Args {
   bool accumulate;
   bool vec;              // rows of out are whole, aligned 16-byte units
 };
-
-// Transposes blocks of U x U units of W words among U neighbouring lanes: unit
-// q of lane l goes to unit (l % U) of lane (l - l % U + q).
-template <int U, int W>
-__device__ __forceinline__ void transpose_units(uint32_t (&v)[U * W], int lane) {
-#pragma unroll
-  for (int s = U / 2; s > 0; s >>= 1) {
-    const bool up = (lane & s) != 0;
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      if (q & s) continue;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        uint32_t& a = v[q * W + w];
-        uint32_t& b = v[(q | s) * W + w];
-        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? a : b, s);
-        if (up) a = got;
-        else b = got;
-      }
-    }
-  }
-}
 
 // Writes 32 columns c0 .. c0 + 31 of the 32 result rows i0 .. i0 + 31, of which
 // this lane holds row i0 + lane.  A lane writing its own row would scatter a
@@ -169,14 +151,30 @@ __device__ __forceinline__ void store_block(const Args& p, int64_t i0, int64_t c
   }
 }
 
+// First row (of CTA `rank`'s half) and column of tile t.
+template <int BN>
+__device__ __forceinline__ void tile_place(const Args& p, int64_t t, int rank, int64_t& i0, int64_t& j0) {
+  const int64_t IT = (p.I + 2 * BM - 1) / (2 * BM), JT = (p.J + BN - 1) / BN;
+  const int64_t g = t / (kGroup * JT), in = t - g * kGroup * JT;
+  const int64_t rows = min(static_cast<int64_t>(kGroup), IT - g * kGroup);
+  i0 = (g * kGroup + in % rows) * 2 * BM + rank * BM;
+  j0 = in / rows * BN;
+}
+
+// Where the sums of 32 rows (quad) x 32 columns (c) of a slice are kept: 16-byte
+// unit q of lane l at 32 q + l.
+__device__ __forceinline__ uint4* partial_block(const Args& p, int64_t item, int rank, int quad, int c) {
+  return reinterpret_cast<uint4*>(p.partial + (item * 2 + rank) * kPartialWords) + (quad * (kSlicedBN / 32) + c) * 256;
+}
+
 template <Op OP, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
              const __grid_constant__ Args p, int32_t* err) {
   using T = OpTraits<OP>;
-  using C = Tile<BN>;
-  constexpr uint32_t kStage = C::template stage<T::b_mn>();
-  constexpr int S = C::template stages<T::b_mn>();
+  static_assert(!T::b_mn || BN % 128 == 0, "whole chunks of an MN-major b per CTA");
+  constexpr uint32_t kStage = Tile<BN>::kStage;
+  constexpr int S = Tile<BN>::S;
   constexpr int32_t kW = ptx::kWaitDense;
   extern __shared__ uint8_t dsmem_raw[];
   const uint32_t raw = ptx::smem_addr(dsmem_raw);
@@ -199,7 +197,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(acc_full(s), 1);
-      ptx::mbar_init(acc_empty(s), 256);     // both CTAs' epilogues
+      ptx::mbar_init(acc_empty(s), 512);     // both CTAs' epilogues
     }
     ptx::mbar_init(drain, 1);
     ptx::mbar_fence_init();
@@ -215,15 +213,23 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int64_t IT = (p.I + 2 * BM - 1) / (2 * BM), JT = (p.J + BN - 1) / BN, tiles = IT * JT;
+  const int64_t tiles = ((p.I + 2 * BM - 1) / (2 * BM)) * ((p.J + BN - 1) / BN);
   const int total = p.blocks * p.parts;     // stages per tile
-  auto place = [&](int64_t t, int64_t& i0, int64_t& j0) {
-    const int64_t g = t / (kGroup * JT), in = t - g * kGroup * JT;
-    const int64_t rows = min(static_cast<int64_t>(kGroup), IT - g * kGroup);
-    i0 = (g * kGroup + in % rows) * 2 * BM + rank * BM;     // this CTA's rows
-    j0 = in / rows * BN;
-  };
+  // work items: whole tiles, then slices of the others
+  const int64_t items = p.whole + (tiles - p.whole) * p.slices;
   const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  auto stages_of = [&](int64_t it, int& r0, int& r1) {
+    r0 = 0;
+    r1 = total;
+    if (it >= p.whole) {
+      const int64_t slice = (it - p.whole) % p.slices;
+      r0 = static_cast<int>(total * slice / p.slices);
+      r1 = static_cast<int>(total * (slice + 1) / p.slices);
+    }
+  };
+  auto place = [&](int64_t it, int64_t& i0, int64_t& j0) {
+    tile_place<BN>(p, it < p.whole ? it : p.whole + (it - p.whole) / p.slices, static_cast<int>(rank), i0, j0);
+  };
 
   if (warp == 0) {
     // ---------------- producer ----------------
@@ -232,11 +238,13 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       // products are issued
       bool ok = true;
       uint32_t n = 0;                       // stages filled so far
-      for (int64_t t = first; t < tiles && ok; t += step) {
+      for (int64_t it = first; it < items && ok; it += step) {
         int64_t i64, j64;
-        place(t, i64, j64);
-        const int i0 = static_cast<int>(i64), j0 = static_cast<int>(j64) + static_cast<int>(rank) * C::rows_b;
-        for (int rb = 0; rb < total; ++rb, ++n) {
+        int rb0, rb1;
+        place(it, i64, j64);
+        stages_of(it, rb0, rb1);
+        const int i0 = static_cast<int>(i64), j0 = static_cast<int>(j64) + static_cast<int>(rank) * (BN / 2);
+        for (int rb = rb0; rb < rb1; ++rb, ++n) {
           const int s = n % S;
           ok = ptx::mbar_wait(empty(s), ((n / S) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitXEmpty));
           if (!ok) break;
@@ -252,7 +260,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
           }
           if constexpr (T::b_mn) {
 #pragma unroll
-            for (int c = 0; c < C::chunks_b; ++c)
+            for (int c = 0; c < BN / 128; ++c)
               ptx::tma_load_3d_pair(sb + c * 8192, &tmap_b, bar, j0 + 64 * c, r0, part);
           } else {
             ptx::tma_load_2d_pair(sb, &tmap_b, bar, r0, j0);
@@ -274,12 +282,14 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         bool ok = true;
         int s = 0;
         uint32_t phase = 0, u = 0;
-        for (int64_t t = first; t < tiles && ok; t += step, ++u) {
+        for (int64_t it = first; it < items && ok; it += step, ++u) {
+          int rb0, rb1;
+          stages_of(it, rb0, rb1);
           const uint32_t acc = tmem + (u & 1) * 256u;
           ok = ptx::mbar_wait(acc_empty(u & 1), ((u >> 1) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitAccEmpty));
           if (!ok) break;
           ptx::tc_fence_after();
-          for (int rb = 0; rb < total; ++rb) {
+          for (int rb = rb0; rb < rb1; ++rb) {
             ok = ptx::mbar_wait(full(s), phase, err, ptx::wait_code(kW, ptx::kWaitFull));
             if (!ok) break;
             ptx::tc_fence_after();
@@ -290,7 +300,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
             constexpr uint64_t da = T::a_mn ? 128 : 2, db = T::b_mn ? 128 : 2;
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              ptx::mma_ss<2, T::i8>(acc, ad + da * k, bd + db * k, idesc, (rb | k) != 0);
+              ptx::mma_ss<2, T::i8>(acc, ad + da * k, bd + db * k, idesc, rb != rb0 || k != 0);
             ptx::mma_commit_pair(empty(s));
             if (++s == S) {
               s = 0;
@@ -309,24 +319,33 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     }
   } else if (warp >= kEpiWarp0) {
     // ---------------- epilogue ----------------
-    const int quad = warp & 3;
+    const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;     // rows, and which blocks of columns
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t u = 0;
-    for (int64_t t = first; t < tiles; t += step, ++u) {
+    for (int64_t it = first; it < items; it += step, ++u) {
       int64_t i0, j0;
-      place(t, i0, j0);
+      place(it, i0, j0);
       const int64_t iw = i0 + quad * 32;      // the warp's first row
       const float rs = OP == kLinearI8 && iw + lane < p.I ? __ldg(p.row_scale + iw + lane) : 0.0f;
       if (!ptx::mbar_wait(acc_full(u & 1), (u >> 1) & 1, err, ptx::wait_code(kW, ptx::kWaitAcc))) break;
       ptx::tc_fence_after();
       const uint32_t acc = tmem + (u & 1) * 256u + lane_addr;
+      const bool sliced = it >= p.whole;
+      const int64_t tail = it - p.whole;
+      const int cols = static_cast<int>(min(static_cast<int64_t>(BN / 32), (p.J - j0 + 31) / 32));
 #pragma unroll 1
-      for (int c = 0; c < BN / 32; ++c) {
-        if (j0 + 32 * c >= p.J) break;
+      for (int c = half; c < cols; c += 2) {
         uint32_t v[32];
         ptx::tmem_ld32(acc + 32 * c, v);
         ptx::tmem_wait_ld(v);
-        if (iw < p.I) store_block<OP>(p, iw, j0 + 32 * c, v, rs, lane);
+        if (iw >= p.I) continue;
+        if (!sliced) {
+          store_block<OP>(p, iw, j0 + 32 * c, v, rs, lane);
+        } else {
+          uint4* dst = partial_block(p, tail, static_cast<int>(rank), quad, c) + lane;
+#pragma unroll
+          for (int q = 0; q < 8; ++q) dst[32 * q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
       }
       ptx::tc_fence_before();
       ptx::mbar_arrive_cluster(ptx::cluster_addr(acc_empty(u & 1), 0));
@@ -339,6 +358,41 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, kTmemCols);
   }
+}
+
+// Adds the slices of the tiles behind the whole ones: a warp for 32 rows x 32
+// columns.
+constexpr int kJoinThreads = 128;
+constexpr int kJoinBlocks = 2 * 4 * (kSlicedBN / 32) * 32 / kJoinThreads;     // per tile
+template <Op OP>
+__global__ void __launch_bounds__(kJoinThreads)
+dense_join_kernel(const __grid_constant__ Args p) {
+  constexpr int BN = kSlicedBN;
+  const int lane = threadIdx.x & 31;
+  const int64_t tail = blockIdx.x / kJoinBlocks;
+  const int block = (blockIdx.x % kJoinBlocks) * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int c = block % (BN / 32), quad = block / (BN / 32) % 4, rank = block / (BN / 32) / 4;
+  int64_t i0, j0;
+  tile_place<BN>(p, p.whole + tail, rank, i0, j0);
+  i0 += quad * 32;
+  j0 += 32 * c;
+  if (i0 >= p.I || j0 >= p.J) return;
+  uint32_t v[32];
+#pragma unroll 2
+  for (int s = 0; s < p.slices; ++s) {
+    const uint4* src = partial_block(p, tail * p.slices + s, rank, quad, c) + lane;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const uint4 w = src[32 * q];
+      const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t& d = v[4 * q + k];
+        d = s == 0 ? x[k] : __float_as_uint(__uint_as_float(d) + __uint_as_float(x[k]));
+      }
+    }
+  }
+  store_block<OP>(p, i0, j0, v, 0.0f, lane);
 }
 
 // A K-major operand: rows of `cols` values (dense in r), box of one stage.
@@ -370,30 +424,22 @@ bool map_mnmajor(CUtensorMap* m, const uint16_t* p, int rank, int64_t slices, in
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Op OP, int BN>
-cudaError_t run(const CUtensorMap& a, const CUtensorMap& b, const Args& p, cudaStream_t stream) {
-  auto kern = dense_kernel<OP, BN>;
-  constexpr size_t smem = Tile<BN>::template smem<OpTraits<OP>::b_mn>();
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), smem);
-  if (e != cudaSuccess) return e;
-  const int64_t tiles = ((p.I + 2 * BM - 1) / (2 * BM)) * ((p.J + BN - 1) / BN);
+int64_t sm_pairs() {
   const int64_t pairs = device_info().num_sms / 2;
-  kern<<<static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), kThreads, smem, stream>>>(a, b, p,
-                                                                                             device_error_word());
-  return cudaGetLastError();
+  return pairs < 1 ? 1 : pairs;
 }
+int64_t tile_count(int64_t I, int64_t J, int bn) { return ((I + 2 * BM - 1) / (2 * BM)) * ((J + bn - 1) / bn); }
 
-// Columns per tile: the width whose tiles fill the SM pairs in whole rounds
-// with the least padding.  A round's time goes with the width down to about
-// 180 columns, below which the loads of a bound it (one B200, int8, 2048 x 5120
-// x 17408: three rounds of 256 take 168 us, three of 192 129 us, five of 128
-// 203 us).  Wide tiles read less of a, so 256 unless a narrower one promises
-// more than 12% (2048 x 17408 x 5120: 256 takes 126 us, 192 133 us for a
-// promise of 6%).
+// Columns per tile of the int8 product: the width whose tiles fill the SM pairs
+// in whole rounds with the least padding.  A round's time goes with the width
+// down to about 180 columns, below which the loads of a bound it (one B200,
+// 2048 x 5120 x 17408: three rounds of 256 take 168 us, three of 192 129 us, five
+// of 128 203 us).  Wide tiles read less of a, so 256 unless a narrower one
+// promises more than 12% (2048 x 17408 x 5120: 256 takes 126 us, 192 133 us for
+// a promise of 6%).
 int tile_columns(int64_t I, int64_t J) {
-  const int64_t pairs = device_info().num_sms / 2, it = (I + 2 * BM - 1) / (2 * BM);
   auto cost = [&](int bn) {
-    return static_cast<double>((it * ((J + bn - 1) / bn) + pairs - 1) / pairs) * (bn > 180 ? bn : 180);
+    return static_cast<double>((tile_count(I, J, bn) + sm_pairs() - 1) / sm_pairs()) * (bn > 180 ? bn : 180);
   };
   int best = 256;
   for (int bn : {192, 128})
@@ -401,13 +447,55 @@ int tile_columns(int64_t I, int64_t J) {
   return best;
 }
 
-template <Op OP>
-cudaError_t run_bn(int bn, const CUtensorMap& a, const CUtensorMap& b, const Args& p, cudaStream_t stream) {
-  switch (bn) {
-    case 128: return run<OP, 128>(a, b, p, stream);
-    case 192: return run<OP, 192>(a, b, p, stream);
-    default: return run<OP, 256>(a, b, p, stream);
+// How the tiles of a bf16 product run (always 256 wide: a half of 192 columns of
+// an MN-major b would be one and a half chunks, loaded as two): `whole` of them in
+// rounds of one per pair of SMs, the rest in slices.  A stage takes a pair
+// about 0.38 us, leaving the sums of slices and adding them about 10 us (one
+// B200, grad_x of 2048 x 17408 x 5120: 330 us with 192-wide tiles in three
+// rounds, 262 us with two rounds of 256 and 12 tiles in six slices).
+struct Plan {
+  int64_t tiles, whole;
+  int slices;
+};
+Plan plan_tiles(int64_t I, int64_t J, int64_t stages) {
+  const int64_t pairs = sm_pairs(), tiles = tile_count(I, J, kSlicedBN), rest = tiles % pairs;
+  Plan p{tiles, tiles, 1};
+  if (rest == 0) return p;
+  double best = static_cast<double>(stages) * 0.38;
+  for (int64_t s = 2; s * rest <= pairs && s * 4 <= stages; ++s) {
+    const double us = static_cast<double>((stages + s - 1) / s) * 0.38 + 10.0;
+    if (us < best) {
+      best = us;
+      p.slices = static_cast<int>(s);
+    }
   }
+  if (p.slices > 1) p.whole = tiles - rest;
+  return p;
+}
+
+template <Op OP, int BN>
+cudaError_t run(const CUtensorMap& a, const CUtensorMap& b, Args p, const Plan& plan, cudaStream_t stream) {
+  auto kern = dense_kernel<OP, BN>;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Tile<BN>::kSmem);
+  if (e != cudaSuccess) return e;
+  p.whole = plan.whole;
+  p.slices = plan.slices;
+  const int64_t items = plan.whole + (plan.tiles - plan.whole) * plan.slices, pairs = sm_pairs();
+  kern<<<static_cast<unsigned>(2 * (items < pairs ? items : pairs)), kThreads, Tile<BN>::kSmem, stream>>>(
+      a, b, p, device_error_word());
+  return cudaGetLastError();
+}
+
+template <Op OP>
+cudaError_t run_sliced(const CUtensorMap& a, const CUtensorMap& b, Args p, void* ws, cudaStream_t stream) {
+  const Plan plan = plan_tiles(p.I, p.J, static_cast<int64_t>(p.blocks) * p.parts);
+  p.partial = static_cast<uint32_t*>(ws);
+  const cudaError_t e = run<OP, kSlicedBN>(a, b, p, plan, stream);
+  if (e != cudaSuccess || plan.slices == 1) return e;
+  p.whole = plan.whole;
+  p.slices = plan.slices;
+  dense_join_kernel<OP><<<static_cast<unsigned>((plan.tiles - plan.whole) * kJoinBlocks), kJoinThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 bool whole16(const void* out, int64_t row_bytes) {
@@ -416,34 +504,68 @@ bool whole16(const void* out, int64_t row_bytes) {
 
 }  // namespace
 
+size_t dense_workspace_bytes(int64_t I, int64_t J, int64_t stages) {
+  const Plan p = plan_tiles(I, J, stages);
+  if (p.slices == 1) return 0;
+  return static_cast<size_t>(p.tiles - p.whole) * static_cast<size_t>(p.slices) * 2 * kPartialWords * 4;
+}
+
+int64_t dense_stages(int64_t depth) { return (depth + 63) / 64; }
+
 cudaError_t launch_dense_i8(const uint8_t* a, const uint8_t* b, const float* sx, const float* scales, int shift,
                             int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream) {
   const int64_t stride = stride_i8(K);
-  CUtensorMap ma, mb;
   const int bn = tile_columns(M, N);
+  CUtensorMap ma, mb;
   if (!map_kmajor(&ma, a, true, M, stride, stride, BM) || !map_kmajor(&mb, b, true, N, stride, stride, bn / 2))
     return cudaErrorInvalidValue;
-  Args p{M, N, static_cast<int>((K + 127) / 128), 1, y, sx, scales, shift, false, whole16(y, 2 * N)};
-  return run_bn<kLinearI8>(bn, ma, mb, p, stream);
+  Args p{};
+  p.I = M;
+  p.J = N;
+  p.blocks = static_cast<int>((K + 127) / 128);
+  p.parts = 1;
+  p.out = y;
+  p.row_scale = sx;
+  p.col_scale = scales;
+  p.shift = shift;
+  p.vec = whole16(y, 2 * N);
+  const int64_t tiles = tile_count(M, N, bn);
+  const Plan plan{tiles, tiles, 1};
+  switch (bn) {
+    case 128: return run<kLinearI8, 128>(ma, mb, p, plan, stream);
+    case 192: return run<kLinearI8, 192>(ma, mb, p, plan, stream);
+    default: return run<kLinearI8, 256>(ma, mb, p, plan, stream);
+  }
 }
 
 cudaError_t launch_dense_grad_x(const uint16_t* dy, const uint16_t* w, int64_t M, int64_t N, int64_t K, uint16_t* dx,
-                                cudaStream_t stream) {
+                                void* ws, cudaStream_t stream) {
   CUtensorMap ma, mb;
   if (!map_kmajor(&ma, dy, false, M, N, 2 * stride_bf16(N), BM) || !map_mnmajor(&mb, w, 3, 1, N, K))
     return cudaErrorInvalidValue;
-  Args p{M, K, static_cast<int>((N + 63) / 64), 1, dx, nullptr, nullptr, 0, false, whole16(dx, 2 * K)};
-  return run_bn<kGradX>(tile_columns(M, K), ma, mb, p, stream);
+  Args p{};
+  p.I = M;
+  p.J = K;
+  p.blocks = static_cast<int>(dense_stages(N));
+  p.parts = 1;
+  p.out = dx;
+  p.vec = whole16(dx, 2 * K);
+  return run_sliced<kGradX>(ma, mb, p, ws, stream);
 }
 
 cudaError_t launch_dense_grad_w(const uint16_t* dy, const uint16_t* x, int parts, int64_t M, int64_t N, int64_t K,
-                                void* dw, bool f32, bool accumulate, cudaStream_t stream) {
+                                void* dw, bool f32, bool accumulate, void* ws, cudaStream_t stream) {
   CUtensorMap ma, mb;
   if (!map_mnmajor(&ma, dy, 2, 1, M, N) || !map_mnmajor(&mb, x, 3, parts, M, K)) return cudaErrorInvalidValue;
-  Args p{N, K, static_cast<int>((M + 63) / 64), parts, dw, nullptr, nullptr, 0, accumulate,
-         whole16(dw, (f32 ? 4 : 2) * K)};
-  const int bn = tile_columns(N, K);
-  return f32 ? run_bn<kGradWF32>(bn, ma, mb, p, stream) : run_bn<kGradWBf16>(bn, ma, mb, p, stream);
+  Args p{};
+  p.I = N;
+  p.J = K;
+  p.blocks = static_cast<int>(dense_stages(M));
+  p.parts = parts;
+  p.out = dw;
+  p.accumulate = accumulate;
+  p.vec = whole16(dw, (f32 ? 4 : 2) * K);
+  return f32 ? run_sliced<kGradWF32>(ma, mb, p, ws, stream) : run_sliced<kGradWBf16>(ma, mb, p, ws, stream);
 }
 
 }  // namespace mpw

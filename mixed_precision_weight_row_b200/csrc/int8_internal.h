@@ -47,11 +47,15 @@ cudaError_t launch_gemm_i8(const uint8_t* xq, const float* sx, const uint8_t* pa
 //   y[m, n] = bf16(s_n * sx_m * (sum_k a[m, k] b[n, k]) / 2^shift), a and b signed bytes
 cudaError_t launch_dense_i8(const uint8_t* a, const uint8_t* b, const float* sx, const float* scales, int shift,
                             int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream);
+// The gradients take a workspace (dense_workspace_bytes of the result's rows
+// and columns and of the stages of the summed axis; unprepared).
+size_t dense_workspace_bytes(int64_t I, int64_t J, int64_t stages);
+int64_t dense_stages(int64_t depth);
 //   dx[m, k] = bf16(sum_n dy[m, n] w[n, k])
 cudaError_t launch_dense_grad_x(const uint16_t* dy, const uint16_t* w, int64_t M, int64_t N, int64_t K, uint16_t* dx,
-                                cudaStream_t stream);
+                                void* ws, cudaStream_t stream);
 //   dw[n, k] (+)= sum_m dy[m, n] (x[m, k] [+ x[M + m, k] with parts == 2])
 cudaError_t launch_dense_grad_w(const uint16_t* dy, const uint16_t* x, int parts, int64_t M, int64_t N, int64_t K,
-                                void* dw, bool f32, bool accumulate, cudaStream_t stream);
+                                void* dw, bool f32, bool accumulate, void* ws, cudaStream_t stream);
 
 }  // namespace mpw

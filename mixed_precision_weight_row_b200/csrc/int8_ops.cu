@@ -15,6 +15,7 @@
 #include "expand.cuh"
 #include "int8_expand.cuh"
 #include "int8_internal.h"
+#include "lane_units.cuh"
 #include "mpw_internal.h"
 #include "tc_ptx.cuh"
 
@@ -106,22 +107,45 @@ __device__ __forceinline__ void load_group(const uint32_t* row, int g, int rw, u
   w[B] = 0u;
 }
 
-// One thread per (row, 32-code group).
+// The group of element idx of N x G, or nothing past the end.
+struct Group {
+  int64_t n;
+  int g;
+  bool in;
+  __device__ Group(int64_t idx, int64_t total, int G) : n(idx / G), g(static_cast<int>(idx - n * G)), in(idx < total) {}
+};
+
+// Stores U 16-byte units per lane to its own dst (units q < have); the lanes of a
+// group of U change units first, so that they write one lane's units side by
+// side (a lane writing its own leaves half a sector at a time).
+template <int U>
+__device__ __forceinline__ void store_units(uint32_t (&o)[4 * U], uint4* dst, int have, int lane) {
+  transpose_units<U, 4>(o, lane);
+  const int q = lane % U, base = lane - q;
+#pragma unroll
+  for (int t = 0; t < U; ++t) {
+    uint4* d = reinterpret_cast<uint4*>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), base + t));
+    const int h = __shfl_sync(0xffffffffu, have, base + t);
+    if (q < h) d[q] = make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
+  }
+}
+
+// One thread per (row, 32-code group); whole warps stay in the loop.
 template <int B, bool PAIRED>
 __global__ void __launch_bounds__(kThreads)
 expand_i8_kernel(const uint32_t* __restrict__ packed, int64_t N, int G, int rw, int stride,
                  uint8_t* __restrict__ out) {
   const int64_t total = N * G;
-  for (int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; idx < total;
-       idx += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t n = idx / G;
-    const int g = static_cast<int>(idx - n * G);
-    uint32_t w[B + 1], o[8];
-    load_group<B>(packed + n * rw, g, rw, w);
+  const int lane = threadIdx.x & 31;
+  for (int64_t w0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane; w0 < total;
+       w0 += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const Group e(w0 + lane, total, G);
+    uint32_t w[B + 1] = {}, o[8];
+    if (e.in) load_group<B>(packed + e.n * rw, e.g, rw, w);
     i8::group<B, PAIRED>(w, o);
-    uint4* dst = reinterpret_cast<uint4*>(out + n * stride + 32 * static_cast<int64_t>(g));
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    if (32 * g + 16 < stride) dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    uint4* dst = reinterpret_cast<uint4*>(out + e.n * stride + 32 * static_cast<int64_t>(e.g));
+    store_units<2>(o, dst, !e.in ? 0 : (32 * e.g + 16 < stride ? 2 : 1), lane);
   }
 }
 
@@ -131,14 +155,14 @@ expand_bf16_kernel(const uint32_t* __restrict__ packed, const float* __restrict_
                    int stride, uint16_t* __restrict__ out) {
   constexpr int P = dec::GemmParts<B>::parts;
   const int64_t total = N * G;
-  for (int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; idx < total;
-       idx += static_cast<int64_t>(gridDim.x) * kThreads) {
-    const int64_t n = idx / G;
-    const int g = static_cast<int>(idx - n * G);
-    uint32_t w[B + 1], v[P][16], o[16];
-    load_group<B>(packed + n * rw, g, rw, w);
+  const int lane = threadIdx.x & 31;
+  for (int64_t w0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane; w0 < total;
+       w0 += static_cast<int64_t>(gridDim.x) * kThreads) {
+    const Group e(w0 + lane, total, G);
+    uint32_t w[B + 1] = {}, v[P][16], o[16];
+    if (e.in) load_group<B>(packed + e.n * rw, e.g, rw, w);
     dec::gemm_expand_group<B, PAIRED>(w, v);
-    const float s = __ldg(scales + n);
+    const float s = e.in ? __ldg(scales + e.n) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float a = bf16_lo(v[0][i]), b = bf16_hi(v[0][i]);
@@ -149,10 +173,8 @@ expand_bf16_kernel(const uint32_t* __restrict__ packed, const float* __restrict_
       const __nv_bfloat162 r = __floats2bfloat162_rn(a * s, b * s);
       o[i] = *reinterpret_cast<const uint32_t*>(&r);
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + n * stride + 32 * static_cast<int64_t>(g));
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (32 * g + 8 * i < stride) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    uint4* dst = reinterpret_cast<uint4*>(out + e.n * stride + 32 * static_cast<int64_t>(e.g));
+    store_units<4>(o, dst, e.in ? min(4, (stride - 32 * e.g) >> 3) : 0, lane);
   }
 }
 
