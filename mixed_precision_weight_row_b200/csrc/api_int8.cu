@@ -21,6 +21,8 @@ bool bits_ok(int bits, int most) { return bits >= kMinBits && bits <= most; }
 bool dims_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 1 && N >= 1 && K >= 1 && M <= kMaxDim && N <= kMaxDim && K <= kMaxDim;
 }
+// Result tiles are counted in 32 bits: up to 2^44 results, far beyond any memory.
+bool result_ok(int64_t I, int64_t J) { return I <= (int64_t{1} << 44) / J; }
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
 
 // Canonical 8-bit rows already are rows of signed bytes.
@@ -82,7 +84,7 @@ mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* p
                             size_t workspace_bytes, mpw_stream_t stream) {
   if (!bits_ok(bits, 8)) return MPW_E_UNSUPPORTED_BITS;
   if (xq == nullptr || sx == nullptr || packed == nullptr || scales == nullptr || y == nullptr) return MPW_E_INVALID_ARG;
-  if (!dims_ok(M, N, K) || K > kInt8MaxK || !layout_ok(layout)) return MPW_E_INVALID_ARG;
+  if (!dims_ok(M, N, K) || K > kInt8MaxK || !layout_ok(layout) || !result_ok(M, N)) return MPW_E_INVALID_ARG;
   if (layout == MPW_LAYOUT_PAIRED && K % 32 != 0) return MPW_E_INVALID_ARG;
   if (!aligned(xq, 16) || !aligned(packed, 16) || !aligned(sx, 4) || !aligned(scales, 4) || !aligned(y, 2))
     return MPW_E_MISALIGNED;
@@ -113,7 +115,7 @@ mpw_status mpw_qlinear_grad_x(const uint16_t* dy, const uint8_t* packed, const f
                               mpw_stream_t stream) {
   if (!bits_ok(bits, kMaxBits)) return MPW_E_UNSUPPORTED_BITS;
   if (dy == nullptr || packed == nullptr || scales == nullptr || dx == nullptr) return MPW_E_INVALID_ARG;
-  if (!dims_ok(M, N, K) || !layout_ok(layout)) return MPW_E_INVALID_ARG;
+  if (!dims_ok(M, N, K) || !layout_ok(layout) || !result_ok(M, K)) return MPW_E_INVALID_ARG;
   if (layout == MPW_LAYOUT_PAIRED && K % 32 != 0) return MPW_E_INVALID_ARG;
   if (!dy_aligned(dy, N) || !aligned(packed, 16) || !aligned(scales, 4) || !aligned(dx, 2)) return MPW_E_MISALIGNED;
   const size_t need = mpw_qlinear_grad_x_workspace_bytes(bits, layout, M, N, K);
@@ -140,7 +142,8 @@ mpw_status mpw_qlinear_grad_w_int8(const uint16_t* dy, const uint8_t* xq, const 
                                    int64_t K, void* dW, int dW_type, int accumulate, void* workspace,
                                    size_t workspace_bytes, mpw_stream_t stream) {
   if (dy == nullptr || xq == nullptr || sx == nullptr || dW == nullptr) return MPW_E_INVALID_ARG;
-  if (!dims_ok(M, N, K) || (dW_type != MPW_GRAD_BF16 && dW_type != MPW_GRAD_F32)) return MPW_E_INVALID_ARG;
+  if (!dims_ok(M, N, K) || (dW_type != MPW_GRAD_BF16 && dW_type != MPW_GRAD_F32) || !result_ok(N, K))
+    return MPW_E_INVALID_ARG;
   const bool f32 = dW_type == MPW_GRAD_F32;
   if (accumulate != 0 && !f32) return MPW_E_INVALID_ARG;
   if (!dy_aligned(dy, N) || !aligned(xq, 16) || !aligned(sx, 4) || !aligned(dW, f32 ? 4 : 2)) return MPW_E_MISALIGNED;

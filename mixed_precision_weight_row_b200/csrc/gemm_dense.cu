@@ -71,7 +71,7 @@ struct Args {
   int64_t I, J;          // results
   int blocks;            // stages along r per part
   int parts;             // passes over r, part p reading part p of b
-  int64_t whole;         // tiles done in one piece; those behind them in slices
+  int whole;             // tiles done in one piece; those behind them in slices
   int slices;
   uint32_t* partial;     // sums of slices: [tile - whole][slice][256 rows x BN]
   void* out;             // [I, J]
@@ -82,16 +82,18 @@ struct Args {
   bool vec;              // rows of out are whole, aligned 16-byte units
 };
 
-// Writes 32 columns c0 .. c0 + 31 of the 32 result rows i0 .. i0 + 31, of which
-// this lane holds row i0 + lane.  A lane writing its own row would scatter a
-// store over 32 rows; the values change lanes first, so that neighbouring
-// lanes write neighbouring 16-byte units (rows of whole, aligned units) or
-// neighbouring values (any other rows).
-template <Op OP>
-__device__ __forceinline__ void store_block(const Args& p, int64_t i0, int64_t c0, uint32_t (&v)[32], float rs,
+// Writes C columns c0 .. c0 + C - 1 of the 32 result rows i0 .. i0 + 31, of which
+// this lane holds row i0 + lane (C = 32, or 64 for bf16: 128 bytes of a row
+// either way).  A lane writing its own row would scatter a store over 32
+// rows; the values change lanes first, so that neighbouring lanes write
+// neighbouring 16-byte units (rows of whole, aligned units) or neighbouring
+// values (any other rows).
+template <Op OP, int C>
+__device__ __forceinline__ void store_block(const Args& p, int64_t i0, int64_t c0, uint32_t (&v)[C], float rs,
                                             int lane) {
   const int64_t left = p.J - c0, rows = p.I - i0;
   if constexpr (OP == kGradWF32) {
+    static_assert(C == 32, "fp32 blocks");
     float* out = static_cast<float*>(p.out) + i0 * p.J + c0;
     if (p.vec) {
       transpose_units<8, 4>(v, lane);
@@ -119,46 +121,57 @@ __device__ __forceinline__ void store_block(const Args& p, int64_t i0, int64_t c
     }
   } else {
     if constexpr (OP == kLinearI8) {
-      const float mine = lane < left ? __ldg(p.col_scale + c0 + lane) : 0.0f;
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float cs = __shfl_sync(0xffffffffu, mine, c);
-        v[c] = __float_as_uint(static_cast<float>(static_cast<int32_t>(v[c]) >> p.shift) * cs * rs);
+      for (int h = 0; h < C / 32; ++h) {
+        const float mine = 32 * h + lane < left ? __ldg(p.col_scale + c0 + 32 * h + lane) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float cs = __shfl_sync(0xffffffffu, mine, c);
+          uint32_t& d = v[32 * h + c];
+          d = __float_as_uint(static_cast<float>(static_cast<int32_t>(d) >> p.shift) * cs * rs);
+        }
       }
+    }
+    uint32_t o[C / 2];      // pairs of columns
+#pragma unroll
+    for (int c = 0; c < C / 2; ++c) {
+      const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+      o[c] = *reinterpret_cast<const uint32_t*>(&r);
     }
     uint16_t* out = static_cast<uint16_t*>(p.out) + i0 * p.J + c0;
     if (p.vec) {
-      uint32_t o[16];
+      constexpr int U = C / 8;
+      transpose_units<U, 4>(o, lane);
+      const int q = lane % U, r0 = lane - q;
 #pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
-        o[c] = *reinterpret_cast<const uint32_t*>(&r);
-      }
-      transpose_units<4, 4>(o, lane);
-      const int q = lane & 3, r0 = lane & ~3;
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < U; ++t)
         if (r0 + t < rows && 8 * q < left)
           reinterpret_cast<uint4*>(out + (r0 + t) * p.J)[q] =
               make_uint4(o[4 * t], o[4 * t + 1], o[4 * t + 2], o[4 * t + 3]);
     } else {
-      transpose_units<32, 1>(v, lane);
+      // C / 2 lanes end up with a pair of columns each, of C / 2 rows at a time
+      constexpr int U = C / 2;
+      transpose_units<U, 1>(o, lane);
+      const int q = lane % U, r0 = lane - q;
 #pragma unroll
-      for (int t = 0; t < 32; ++t)
-        if (t < rows && lane < left)
-          out[t * p.J + lane] = __bfloat16_as_ushort(__float2bfloat16_rn(__uint_as_float(v[t])));
+      for (int t = 0; t < U; ++t) {
+        if (r0 + t >= rows) continue;
+        uint16_t* dst = out + (r0 + t) * p.J + 2 * q;
+        if (2 * q < left) dst[0] = static_cast<uint16_t>(o[t]);
+        if (2 * q + 1 < left) dst[1] = static_cast<uint16_t>(o[t] >> 16);
+      }
     }
   }
 }
 
 // First row (of CTA `rank`'s half) and column of tile t.
 template <int BN>
-__device__ __forceinline__ void tile_place(const Args& p, int64_t t, int rank, int64_t& i0, int64_t& j0) {
-  const int64_t IT = (p.I + 2 * BM - 1) / (2 * BM), JT = (p.J + BN - 1) / BN;
-  const int64_t g = t / (kGroup * JT), in = t - g * kGroup * JT;
-  const int64_t rows = min(static_cast<int64_t>(kGroup), IT - g * kGroup);
-  i0 = (g * kGroup + in % rows) * 2 * BM + rank * BM;
-  j0 = in / rows * BN;
+__device__ __forceinline__ void tile_place(const Args& p, int t, int rank, int64_t& i0, int64_t& j0) {
+  const int IT = static_cast<int>((p.I + 2 * BM - 1) / (2 * BM)), JT = static_cast<int>((p.J + BN - 1) / BN);
+  const int g = t / (kGroup * JT), in = t - g * kGroup * JT;
+  const int rows = min(kGroup, IT - g * kGroup);
+  i0 = static_cast<int64_t>(g * kGroup + in % rows) * (2 * BM) + rank * BM;
+  j0 = static_cast<int64_t>(in / rows) * BN;
 }
 
 // Where the sums of 32 rows (quad) x 32 columns (c) of a slice are kept: 16-byte
@@ -213,12 +226,12 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int64_t tiles = ((p.I + 2 * BM - 1) / (2 * BM)) * ((p.J + BN - 1) / BN);
+  const int tiles = static_cast<int>(((p.I + 2 * BM - 1) / (2 * BM)) * ((p.J + BN - 1) / BN));
   const int total = p.blocks * p.parts;     // stages per tile
   // work items: whole tiles, then slices of the others
-  const int64_t items = p.whole + (tiles - p.whole) * p.slices;
-  const int64_t first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  auto stages_of = [&](int64_t it, int& r0, int& r1) {
+  const int items = p.whole + (tiles - p.whole) * p.slices;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+  auto stages_of = [&](int it, int& r0, int& r1) {
     r0 = 0;
     r1 = total;
     if (it >= p.whole) {
@@ -227,7 +240,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       r1 = static_cast<int>(total * (slice + 1) / p.slices);
     }
   };
-  auto place = [&](int64_t it, int64_t& i0, int64_t& j0) {
+  auto place = [&](int it, int64_t& i0, int64_t& j0) {
     tile_place<BN>(p, it < p.whole ? it : p.whole + (it - p.whole) / p.slices, static_cast<int>(rank), i0, j0);
   };
 
@@ -238,7 +251,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       // products are issued
       bool ok = true;
       uint32_t n = 0;                       // stages filled so far
-      for (int64_t it = first; it < items && ok; it += step) {
+      for (int it = first; it < items && ok; it += step) {
         int64_t i64, j64;
         int rb0, rb1;
         place(it, i64, j64);
@@ -282,7 +295,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         bool ok = true;
         int s = 0;
         uint32_t phase = 0, u = 0;
-        for (int64_t it = first; it < items && ok; it += step, ++u) {
+        for (int it = first; it < items && ok; it += step, ++u) {
           int rb0, rb1;
           stages_of(it, rb0, rb1);
           const uint32_t acc = tmem + (u & 1) * 256u;
@@ -322,7 +335,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;     // rows, and which blocks of columns
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t u = 0;
-    for (int64_t it = first; it < items; it += step, ++u) {
+    for (int it = first; it < items; it += step, ++u) {
       int64_t i0, j0;
       place(it, i0, j0);
       const int64_t iw = i0 + quad * 32;      // the warp's first row
@@ -331,20 +344,27 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       ptx::tc_fence_after();
       const uint32_t acc = tmem + (u & 1) * 256u + lane_addr;
       const bool sliced = it >= p.whole;
-      const int64_t tail = it - p.whole;
-      const int cols = static_cast<int>(min(static_cast<int64_t>(BN / 32), (p.J - j0 + 31) / 32));
+      const int tail = it - p.whole;
+      constexpr int C = OP == kGradWF32 ? 32 : 64;      // columns per step
+      const int cols = static_cast<int>(min(static_cast<int64_t>(BN / C), (p.J - j0 + C - 1) / C));
 #pragma unroll 1
       for (int c = half; c < cols; c += 2) {
-        uint32_t v[32];
-        ptx::tmem_ld32(acc + 32 * c, v);
-        ptx::tmem_wait_ld(v);
+        uint32_t v[C];
+#pragma unroll
+        for (int h = 0; h < C / 32; ++h) ptx::tmem_ld32(acc + C * c + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
+#pragma unroll
+        for (int h = 0; h < C / 32; ++h) ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
         if (iw >= p.I) continue;
         if (!sliced) {
-          store_block<OP>(p, iw, j0 + 32 * c, v, rs, lane);
+          store_block<OP, C>(p, iw, j0 + C * c, v, rs, lane);
         } else {
-          uint4* dst = partial_block(p, tail, static_cast<int>(rank), quad, c) + lane;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) dst[32 * q] = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          for (int h = 0; h < C / 32; ++h) {
+            uint4* dst = partial_block(p, tail, static_cast<int>(rank), quad, C / 32 * c + h) + lane;
+            const uint32_t* w = v + 32 * h;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dst[32 * q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+          }
         }
       }
       ptx::tc_fence_before();
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 dense_join_kernel(const __grid_constant__ Args p) {
   constexpr int BN = kSlicedBN;
   const int lane = threadIdx.x & 31;
-  const int64_t tail = blockIdx.x / kJoinBlocks;
+  const int tail = static_cast<int>(blockIdx.x) / kJoinBlocks;
   const int block = (blockIdx.x % kJoinBlocks) * (kJoinThreads / 32) + (threadIdx.x >> 5);
   const int c = block % (BN / 32), quad = block / (BN / 32) % 4, rank = block / (BN / 32) / 4;
   int64_t i0, j0;
@@ -380,7 +400,7 @@ dense_join_kernel(const __grid_constant__ Args p) {
   uint32_t v[32];
 #pragma unroll 2
   for (int s = 0; s < p.slices; ++s) {
-    const uint4* src = partial_block(p, tail * p.slices + s, rank, quad, c) + lane;
+    const uint4* src = partial_block(p, static_cast<int64_t>(tail) * p.slices + s, rank, quad, c) + lane;
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const uint4 w = src[32 * q];
@@ -392,7 +412,7 @@ dense_join_kernel(const __grid_constant__ Args p) {
       }
     }
   }
-  store_block<OP>(p, i0, j0, v, 0.0f, lane);
+  store_block<OP, 32>(p, i0, j0, v, 0.0f, lane);
 }
 
 // A K-major operand: rows of `cols` values (dense in r), box of one stage.
@@ -478,7 +498,7 @@ cudaError_t run(const CUtensorMap& a, const CUtensorMap& b, Args p, const Plan& 
   auto kern = dense_kernel<OP, BN>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Tile<BN>::kSmem);
   if (e != cudaSuccess) return e;
-  p.whole = plan.whole;
+  p.whole = static_cast<int>(plan.whole);
   p.slices = plan.slices;
   const int64_t items = plan.whole + (plan.tiles - plan.whole) * plan.slices, pairs = sm_pairs();
   kern<<<static_cast<unsigned>(2 * (items < pairs ? items : pairs)), kThreads, Tile<BN>::kSmem, stream>>>(
@@ -492,7 +512,7 @@ cudaError_t run_sliced(const CUtensorMap& a, const CUtensorMap& b, Args p, void*
   p.partial = static_cast<uint32_t*>(ws);
   const cudaError_t e = run<OP, kSlicedBN>(a, b, p, plan, stream);
   if (e != cudaSuccess || plan.slices == 1) return e;
-  p.whole = plan.whole;
+  p.whole = static_cast<int>(plan.whole);
   p.slices = plan.slices;
   dense_join_kernel<OP><<<static_cast<unsigned>((plan.tiles - plan.whole) * kJoinBlocks), kJoinThreads, 0, stream>>>(p);
   return cudaGetLastError();

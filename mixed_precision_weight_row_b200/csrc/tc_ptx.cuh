@@ -408,8 +408,11 @@ __device__ __forceinline__ int32_t ld_cluster_s32(uint32_t addr) {
   return v;
 }
 // Arrives on an mbarrier of any CTA of the cluster (an address of cluster_addr).
+// For tensor memory that has been read (tmem_wait_ld, tc_fence_before): a
+// release at cluster scope would also wait for the thread's stores to global
+// memory, which nobody behind this barrier looks at.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // Tile loads into this CTA's shared memory that complete on an mbarrier of
 // either CTA of the pair.
