@@ -30,6 +30,7 @@
 #include "int8_internal.h"
 #include "mpw_internal.h"
 #include "tc_ptx.cuh"
+#include "tile_choice.h"
 
 namespace mpw {
 namespace {
@@ -68,7 +69,7 @@ struct Code {
   // A stage is always read by the same group: were it another one's turn, that
   // group could find the stage's previous fill, not yet complete, to have the
   // parity it waits for.
-  static_assert(SW % G == 0, "whole turns of the groups per ring");
+  static_assert(SW % G == 0 && SA >= G, "whole turns of the groups per ring");
   // the sums of a split tile take the place of the x ring
   static_assert(SX * kXStage >= BM * BN * 4, "room for the sums");
 };
@@ -333,8 +334,6 @@ cudaError_t run(const uint8_t* xq, const float* sx, const uint8_t* packed, const
       return cudaErrorInvalidValue;
   }
   auto kern = gemm_i8_kernel<B, PAIRED, BN>;
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((M + BN - 1) / BN * splits), static_cast<unsigned>((N + BM - 1) / BM));
   cfg.blockDim = dim3(C::kThreads);
@@ -353,45 +352,59 @@ cudaError_t run(const uint8_t* xq, const float* sx, const uint8_t* packed, const
                             static_cast<int>((K + BK - 1) / BK), splits, device_error_word());
 }
 
-// Tokens per tile and K slices per tile, by the time this kernel takes: a CTA
-// spends 0.29 us a block of 128 codes with up to 128 tokens and 0.42 us with
-// 256, 1.7 us to start and end, and joining S slices costs 2 us and S * BN / 128
-// more; the CTAs run in rounds of one per SM.  (One B200; for instance 4096 x
-// 4096, b = 4, 256 tokens: 128 / 1 slice 10.9 us, 256 / 4 13.0, 256 / 1 15.8;
-// 1024 x 5120, b = 5, 128 tokens: 64 / 4 6.9, 128 / 4 7.9, 128 / 1 14.1.
-// Clusters of eight did not all run at once: 64 / 8 14.2.)  A smaller tile or
-// more slices only for 7% less, since they also read more.
-void choose_tile(int64_t M, int64_t N, int64_t blocks, int* bn, int* splits) {
-  const int64_t sms = device_info().num_sms, rows = (N + BM - 1) / BM;
-  int widest = 16;
-  while (widest < 256 && widest < M) widest *= 2;
-  double best = 0.0;
-  for (int w = widest; w >= 16 && w >= widest / 4; w /= 2)
-    for (int s = 1; s <= 4 && s * 4 <= blocks; s *= 2) {
-      const int64_t ctas = (M + w - 1) / w * rows * s;
-      const double us = static_cast<double>((ctas + sms - 1) / sms) *
-                        (static_cast<double>((blocks + s - 1) / s) * (w == 256 ? 0.42 : 0.29) + 1.7 +
-                         (s > 1 ? 2.0 + s * w / 128.0 : 0.0));
-      if (best == 0.0 || us < 0.93 * best) {
-        best = us;
-        *bn = w;
-        *splits = s;
-      }
+// Slices for tiles of BN tokens and the time they promise.  (One B200, a block 0.29 us
+// with up to 128 tokens and 0.42 us with 256; for instance 4096 x 4096, b = 4, 256
+// tokens: 128-token tiles 10.9 us, 256 in four slices 13.0, 256 whole 15.8; 1024 x
+// 5120, b = 5, 128 tokens: tiles of 64 in four slices 6.9, 128 in four 7.9, 128 whole
+// 14.1.)
+template <int B, bool PAIRED, int BN>
+cudaError_t slices(int64_t M, int64_t N, int64_t K, int* s, double* us) {
+  using C = Code<B, BN>;
+  auto kern = gemm_i8_kernel<B, PAIRED, BN>;
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM);
+  if (e != cudaSuccess) return e;
+  const ClusterCapacity& cap = cluster_capacity(kern, C::kThreads, C::SMEM);
+  const int64_t tiles = (M + BN - 1) / BN * ((N + BM - 1) / BM), blocks = (K + BK - 1) / BK;
+  *s = 1;
+  *us = 0.0;
+  for (int i = 1; i <= kMaxSlices && (i == 1 || i * 4 <= blocks); ++i) {
+    if (cap.ctas[i] == 0) continue;
+    const double t = tile_time(tiles * i, cap.ctas[i], blocks, i, BN, BN == 256 ? 0.42 : 0.29, 1.7);
+    if (*us == 0.0 || t < 0.95 * *us) {
+      *us = t;
+      *s = i;
     }
+  }
+  return cudaSuccess;
+}
+
+// The widest tile that M fills, or one or two halvings of it where those promise
+// 7% less (they read more).
+template <int B, bool PAIRED, int BN, int HALVINGS>
+cudaError_t run_tile(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int64_t M,
+                     int64_t N, int64_t K, uint16_t* y, cudaStream_t stream) {
+  int s = 1;
+  double us = 0.0;
+  const cudaError_t e = slices<B, PAIRED, BN>(M, N, K, &s, &us);
+  if (e != cudaSuccess) return e;
+  if constexpr (HALVINGS > 0 && BN > 16) {
+    int s2 = 1;
+    double us2 = 0.0;
+    const cudaError_t e2 = slices<B, PAIRED, BN / 2>(M, N, K, &s2, &us2);
+    if (e2 != cudaSuccess) return e2;
+    if (us2 < 0.93 * us) return run_tile<B, PAIRED, BN / 2, HALVINGS - 1>(xq, sx, packed, scales, M, N, K, y, stream);
+  }
+  return run<B, PAIRED, BN>(xq, sx, packed, scales, M, N, K, y, s, stream);
 }
 
 template <int B, bool PAIRED>
 cudaError_t run_bn(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int64_t M,
                    int64_t N, int64_t K, uint16_t* y, cudaStream_t stream) {
-  int bn = 16, s = 1;
-  choose_tile(M, N, (K + BK - 1) / BK, &bn, &s);
-  switch (bn) {
-    case 16: return run<B, PAIRED, 16>(xq, sx, packed, scales, M, N, K, y, s, stream);
-    case 32: return run<B, PAIRED, 32>(xq, sx, packed, scales, M, N, K, y, s, stream);
-    case 64: return run<B, PAIRED, 64>(xq, sx, packed, scales, M, N, K, y, s, stream);
-    case 128: return run<B, PAIRED, 128>(xq, sx, packed, scales, M, N, K, y, s, stream);
-    default: return run<B, PAIRED, 256>(xq, sx, packed, scales, M, N, K, y, s, stream);
-  }
+  if (M <= 16) return run_tile<B, PAIRED, 16, 0>(xq, sx, packed, scales, M, N, K, y, stream);
+  if (M <= 32) return run_tile<B, PAIRED, 32, 1>(xq, sx, packed, scales, M, N, K, y, stream);
+  if (M <= 64) return run_tile<B, PAIRED, 64, 2>(xq, sx, packed, scales, M, N, K, y, stream);
+  if (M <= 128) return run_tile<B, PAIRED, 128, 2>(xq, sx, packed, scales, M, N, K, y, stream);
+  return run_tile<B, PAIRED, 256, 2>(xq, sx, packed, scales, M, N, K, y, stream);
 }
 
 template <int B>

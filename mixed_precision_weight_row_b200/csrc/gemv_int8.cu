@@ -55,27 +55,6 @@ __host__ __device__ constexpr uint32_t x_bytes(int MT, int K) {
   return static_cast<uint32_t>(MT) * static_cast<uint32_t>((K + 31) / 32) * 32u;
 }
 
-template <int B>
-__device__ __forceinline__ void lds_group(const uint8_t* p, uint32_t (&w)[B + 1]) {
-  if constexpr (B % 4 == 0) {
-#pragma unroll
-    for (int i = 0; i < B / 4; ++i) {
-      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
-      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
-    }
-  } else if constexpr (B % 2 == 0) {
-#pragma unroll
-    for (int i = 0; i < B / 2; ++i) {
-      const uint2 v = reinterpret_cast<const uint2*>(p)[i];
-      w[2 * i] = v.x; w[2 * i + 1] = v.y;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < B; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
-  }
-  w[B] = 0u;
-}
-
 // MT: tokens (M <= MT, the others are zero), R: rows per unit.
 template <int B, bool PAIRED, int MT, int R>
 __global__ void __launch_bounds__(kMaxWarps * 32, 2)
@@ -157,7 +136,7 @@ gemv_i8_kernel(const __grid_constant__ Args p, int32_t* err) {
         // a last group may reach past its row (and a last unit hold fewer than
         // R rows): what is read there meets zeros of x or is not written
         uint32_t w[B + 1];
-        lds_group<B>(w0 + r * seg_bytes + (g - g0) * 4 * B, w);
+        i8::lds_group<B>(w0 + r * seg_bytes + (g - g0) * 4 * B, w);
         i8::group_ordered<B, PAIRED>(w, o[r]);
       }
 #pragma unroll

@@ -23,6 +23,29 @@ struct Just {
   static constexpr uint32_t kMask = ((0xFFu << (8 - B)) & 0xFFu) * 0x01010101u;
 };
 
+// The B words of a group from shared memory (w[B] = 0), in the widest loads its
+// alignment allows.
+template <int B>
+__device__ __forceinline__ void lds_group(const uint8_t* p, uint32_t (&w)[B + 1]) {
+  if constexpr (B % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < B / 4; ++i) {
+      const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+    }
+  } else if constexpr (B % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < B / 2; ++i) {
+      const uint2 v = reinterpret_cast<const uint2*>(p)[i];
+      w[2 * i] = v.x; w[2 * i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < B; ++i) w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+  }
+  w[B] = 0u;
+}
+
 // Shift by a compile-time amount, left when positive.
 template <int S>
 __device__ __forceinline__ uint32_t shift(uint32_t v) {

@@ -42,6 +42,12 @@ bool gemm_i8_fits(int64_t M, int64_t N);
 cudaError_t launch_gemm_i8(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int bits,
                            int layout, int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream);
 
+// gradx_fused.cu: the gradient of x for up to a few hundred tokens, packed rows
+// expanded on the way to the tensor cores; dy rows of stride_bf16(N).
+bool gradx_fused_fits(int bits, int64_t M, int64_t N, int64_t K);
+cudaError_t launch_gradx_fused(const uint16_t* dy, const uint8_t* packed, const float* scales, int bits, int layout,
+                               int64_t M, int64_t N, int64_t K, uint16_t* dx, cudaStream_t stream);
+
 // gemm_dense.cu: products of operands laid out for TMA (rows of a stride that
 // is a multiple of 16 bytes, 16-byte aligned).
 //   y[m, n] = bf16(s_n * sx_m * (sum_k a[m, k] b[n, k]) / 2^shift), a and b signed bytes

@@ -17,6 +17,7 @@
 #include "int8_internal.h"
 #include "lane_units.cuh"
 #include "mpw_internal.h"
+#include "scale_pair.cuh"
 #include "tc_ptx.cuh"
 
 namespace mpw {
@@ -163,15 +164,18 @@ expand_bf16_kernel(const uint32_t* __restrict__ packed, const float* __restrict_
     if (e.in) load_group<B>(packed + e.n * rw, e.g, rw, w);
     dec::gemm_expand_group<B, PAIRED>(w, v);
     const float s = e.in ? __ldg(scales + e.n) : 0.0f;
+    uint32_t hi, lo;
+    dec::split_scale(s, hi, lo);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float a = bf16_lo(v[0][i]), b = bf16_hi(v[0][i]);
-      if constexpr (P == 2) {
-        a += bf16_lo(v[1][i]);   // exact: the code has at most 15 bits
-        b += bf16_hi(v[1][i]);
+      if constexpr (P == 1) {
+        o[i] = dec::scale_pair(v[0][i], hi, lo);
+      } else {
+        // the parts' sum is exact in fp32: the code has at most 15 bits
+        const __nv_bfloat162 r = __floats2bfloat162_rn((bf16_lo(v[0][i]) + bf16_lo(v[1][i])) * s,
+                                                       (bf16_hi(v[0][i]) + bf16_hi(v[1][i])) * s);
+        o[i] = *reinterpret_cast<const uint32_t*>(&r);
       }
-      const __nv_bfloat162 r = __floats2bfloat162_rn(a * s, b * s);
-      o[i] = *reinterpret_cast<const uint32_t*>(&r);
     }
     uint4* dst = reinterpret_cast<uint4*>(out + e.n * stride + 32 * static_cast<int64_t>(e.g));
     store_units<4>(o, dst, e.in ? min(4, (stride - 32 * e.g) >> 3) : 0, lane);

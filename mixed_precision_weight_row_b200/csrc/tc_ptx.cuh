@@ -68,7 +68,7 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint32_t bar, uint32_t parit
 // 100 * kernel + place.  The first one stays until the word is read.
 enum WaitKernel : int32_t {
   kWaitGemvTma = 1, kWaitGemvTc = 2, kWaitGemm = 3, kWaitGemvSk = 4, kWaitGemmFp8 = 5, kWaitGemvPass = 6,
-  kWaitDense = 7, kWaitGemmI8 = 8, kWaitGemvI8 = 9
+  kWaitDense = 7, kWaitGemmI8 = 8, kWaitGemvI8 = 9, kWaitGradX = 10
 };
 enum WaitPlace : int32_t {
   kWaitXEmpty = 1,    // x producer: a free x stage

@@ -253,10 +253,22 @@ def test_grad_x(mpw, M, N, K, b):
     _check_grad_x(mpw, M, N, K, b, "canonical")
 
 
+@pytest.mark.parametrize("M", [50, 700])
 @pytest.mark.parametrize("layout", ["canonical", "paired"])
 @pytest.mark.parametrize("b", list(range(4, 16)))
-def test_grad_x_every_width(mpw, b, layout):
-    _check_grad_x(mpw, 50, 200, 288, b, layout)
+def test_grad_x_every_width(mpw, b, layout, M):
+    _check_grad_x(mpw, M, 200, 288, b, layout)
+
+
+@pytest.mark.parametrize("M", [1, 2, 7, 16, 32, 33, 64, 65, 100, 128, 129, 200, 256, 257, 400, 512, 513, 1100])
+def test_grad_x_every_token_count(mpw, M):
+    _check_grad_x(mpw, M, 1300, 520, 6, "canonical")
+
+
+@pytest.mark.parametrize("M", [3, 40, 150, 600])
+@pytest.mark.parametrize("b", [4, 7, 8])
+def test_grad_x_many_rows(mpw, M, b):
+    _check_grad_x(mpw, M, 17408, 72, b, "canonical")
 
 
 def _check_grad_w(mpw, M, N, K, fp32, accumulate=False):
@@ -284,7 +296,13 @@ def test_grad_w(mpw, M, N, K, fp32):
     _check_grad_w(mpw, M, N, K, fp32)
 
 
-@pytest.mark.parametrize("M,N,K", [(16, 64, 128), (130, 257, 333), (300, 130, 1280)])
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("M,N,K", [(4100, 300, 500), (8200, 40, 72), (1, 300, 17408)])
+def test_grad_w_many_tokens_and_one(mpw, M, N, K, fp32):
+    _check_grad_w(mpw, M, N, K, fp32)
+
+
+@pytest.mark.parametrize("M,N,K", [(16, 64, 128), (130, 257, 333), (300, 130, 1280), (4100, 300, 500)])
 def test_grad_w_accumulates(mpw, M, N, K):
     _check_grad_w(mpw, M, N, K, True, accumulate=True)
 
@@ -496,7 +514,7 @@ def test_refusals(mpw):
     with pytest.raises(TypeError):
         mpw.qlinear_grad_w_int8(dy, xq, sx, K, dtype=torch.float16)
     with pytest.raises(ValueError):
-        mpw.qlinear_grad_x(dy, packed, scales, 6, K, workspace=torch.empty((16,), dtype=torch.uint8, device="cuda"))
+        mpw.qlinear_grad_w_int8(dy, xq, sx, K, workspace=torch.empty((16,), dtype=torch.uint8, device="cuda"))
     p9, s9 = mpw.quantize_pack(torch.randn(N, K, device="cuda"), 9)
     with pytest.raises(mpw.MPWError) as e:
         mpw.qlinear_int8(x, p9, s9, 9)

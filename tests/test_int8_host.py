@@ -43,11 +43,11 @@ def test_grad_x_validation():
     for b in (3, 16):
         assert _gx(bits=b) == BITS
     for kw in [dict(dy=0), dict(packed=0), dict(scales=0), dict(dx=0), dict(M=0), dict(N=0), dict(K=0), dict(layout=3),
-               dict(layout=1, K=48), dict(M=1 << 30), dict(ws=0),
-               dict(nb=mpw.lib.mpw_qlinear_grad_x_workspace_bytes(6, 0, 64, 32, 64) - 1)]:
+               dict(layout=1, K=48), dict(M=1 << 30), dict(ws=0, M=4000),
+               dict(M=4000, nb=mpw.lib.mpw_qlinear_grad_x_workspace_bytes(6, 0, 4000, 32, 64) - 1)]:
         assert _gx(**kw) == INV, kw
     for kw in [dict(dy=A + 2), dict(dy=A + 1, N=33), dict(packed=B + 8), dict(scales=C + 2), dict(dx=D + 1),
-               dict(ws=W + 8)]:
+               dict(ws=W + 8, M=4000)]:
         assert _gx(**kw) == ALIGN, kw
 
 
