@@ -12,7 +12,9 @@
 //     TMA into a ring of SW stages;
 //   * A: groups of four converter warps take the blocks in turn; a thread
 //     expands 32 codes of a row to bf16, scales them and writes 64 bytes into
-//     the 128-byte swizzle (two chunks of 64 k x 64 rows, 16 KB);
+//     the 128-byte swizzle (two chunks of 64 k x 64 rows, 16 KB).  The codes of a
+//     canonical group are left in the order that takes the fewest operations;
+//     the writer of dx knows which input a lane holds;
 //   * B: BN tokens x 64 values of dy by TMA;
 //   * D: fp32, BN columns of tensor memory.
 // A cluster of S CTAs shares a tile when the tiles do not fill the SMs: each
@@ -49,7 +51,25 @@ struct Code {
   static constexpr uint32_t kWStage = BK * PITCH;
   static constexpr int SX = BN == 256 ? 3 : 4;
   static constexpr int SW = BN == 256 ? 4 : 8;
-  static constexpr uint32_t kCols = BN < 32 ? 32 : BN;        // tensor memory
+  static constexpr uint32_t kCols = BN;                       // tensor memory
+  static constexpr CUtensorMapSwizzle WSWZ =
+      B == 8 ? CU_TENSOR_MAP_SWIZZLE_128B : (B == 4 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_NONE);
+  // the B words of group g of row r of a weight stage
+  static __device__ __forceinline__ void load(const uint8_t* stage, int r, int g, uint32_t (&w)[B + 1]) {
+    if constexpr (B == 8) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + 16 * ((2 * g + u) ^ (r & 7)));
+        w[4 * u] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
+      }
+      w[8] = 0u;
+    } else if constexpr (B == 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + 16 * (g ^ ((r >> 1) & 3)));
+      w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w; w[4] = 0u;
+    } else {
+      i8::lds_group<B>(stage + r * PITCH + g * 4 * B, w);
+    }
+  }
   // A stage is always read, and one of A always written, by groups that are at
   // most one fill behind: whole turns of the groups per weight ring, and a ring
   // of A of at least one turn.
@@ -59,6 +79,12 @@ struct Code {
   // the sums of a split tile take the place of the rings of A and B
   static_assert(SA * kAStage + SX * kXStage >= BM * BN * 4, "room for the sums");
 };
+
+// The input that lane r of a tile holds.
+template <bool PAIRED>
+__device__ __forceinline__ int input_of(int r) {
+  return PAIRED ? r : (r & ~31) + ((r & 31) >> 1) + 16 * (r & 1);
+}
 
 template <int B, bool PAIRED, int BN>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -175,15 +201,22 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
   } else if (warp >= kConvWarp0) {
     // ---------------- converters ----------------
     const int wg = (warp - kConvWarp0) >> 2;       // which blocks
-    const int t128 = (warp & 3) * 32 + lane;
-    const int g = t128 & 3, r0 = t128 >> 2;        // 32-code group of the tile; rows r0 and r0 + 32 of the block
+    // 32-code group of the tile, and rows r0 and r0 + 32 of the block: the eight
+    // lanes that store together hold eight rows, whose swizzled units cover
+    // every bank once
+    const int g = lane >> 3, r0 = (warp & 3) * 8 + (lane & 7);
+    auto scale_of = [&](int b, int h) {
+      const int64_t n = static_cast<int64_t>(nb0 + b) * BK + r0 + 32 * h;
+      return b < nbs && n < N ? __ldg(scales + n) : 0.0f;
+    };
+    float next[2] = {scale_of(wg, 0), scale_of(wg, 1)};     // read a turn ahead
     for (int b = wg; b < nbs; b += kGroups) {
       const int ws = b % SW, sa = b % SA;
       uint32_t s2[2][2];                           // the rows' scales as pairs of bf16, high and low part
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int64_t n = static_cast<int64_t>(nb0 + b) * BK + r0 + 32 * h;
-        dec::split_scale(n < N ? __ldg(scales + n) : 0.0f, s2[h][0], s2[h][1]);
+        dec::split_scale(next[h], s2[h][0], s2[h][1]);
+        next[h] = scale_of(b + kGroups, h);
       }
       ok = ptx::mbar_wait(full_w(ws), (b / SW) & 1, err, ptx::wait_code(kW, ptx::kWaitWFull));
       if (!ok) break;
@@ -192,8 +225,14 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t w[B + 1], v[dec::GemmParts<B>::parts][16];
-        i8::lds_group<B>(stage + (r0 + 32 * h) * C::PITCH + g * 4 * B, w);
-        dec::gemm_expand_group<B, PAIRED>(w, v);
+        C::load(stage, r0 + 32 * h, g, w);
+        if constexpr (PAIRED) {
+          dec::gemm_expand_group<B, true>(w, v);
+        } else {
+          uint32_t z[B + 1];
+          i8::halves_of<B>(w, z);
+          dec::gemm_expand_group<B, true>(z, v);
+        }
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[h][i] = dec::scale_pair(v[0][i], s2[h][0], s2[h][1]);
       }
@@ -202,20 +241,13 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
       ok = ptx::mbar_wait(empty_a(sa), ((b / SA) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitAEmpty));
       if (!ok) break;
       uint8_t* a = gsmem + sa * kAStage + (g >> 1) * (BK * 128);
-      const bool odd_chunk = (g >> 1) != 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = r0 + 32 * h;
-        // 16-byte units of the row, the second chunk's in another order, so that
-        // the eight lanes that store together hit every bank once
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i0 = 4 * j, i1 = 4 * (j ^ 2);
-          const uint4 u = odd_chunk ? make_uint4(o[h][i1], o[h][i1 + 1], o[h][i1 + 2], o[h][i1 + 3])
-                                    : make_uint4(o[h][i0], o[h][i0 + 1], o[h][i0 + 2], o[h][i0 + 3]);
-          const int unit = 4 * (g & 1) + (odd_chunk ? j ^ 2 : j);
-          *reinterpret_cast<uint4*>(a + r * 128 + 16 * (unit ^ (r & 7))) = u;
-        }
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4*>(a + r * 128 + 16 * ((4 * (g & 1) + j) ^ (r & 7))) =
+              make_uint4(o[h][4 * j], o[h][4 * j + 1], o[h][4 * j + 2], o[h][4 * j + 3]);
       }
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(full_a(sa));
@@ -227,7 +259,7 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
     if (ok) ok = ptx::mbar_wait(acc_full, 0, err, ptx::wait_code(kW, ptx::kWaitAcc));
     if (ok) {
       ptx::tc_fence_after();
-      const int64_t k = k0 + r;
+      const int64_t k = k0 + input_of<PAIRED>(r);
       for (int c = wg; c < BN / 32; c += kGroups) {
         uint32_t v[32];
         ptx::tmem_ld32(tmem + lane_addr + c * 32, v);
@@ -250,7 +282,7 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
       // reads of one slice's sums overlap
       constexpr int E = 8;
       const int r = threadIdx.x & 127;
-      const int64_t k = k0 + r;
+      const int64_t k = k0 + input_of<PAIRED>(r);
       const int t1 = min(BN, M - m0);
       for (int t0 = E * (part * kGroups + ((warp - kConvWarp0) >> 2)); t0 < t1; t0 += E * splits * kGroups) {
         float sum[E];
@@ -304,7 +336,7 @@ cudaError_t run(const uint16_t* dy, const uint8_t* packed, const float* scales, 
     const cuuint64_t strides[1] = {static_cast<cuuint64_t>(rb)};
     const cuuint32_t box[2] = {16 * B, BK};
     if (encode(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(packed), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, C::WSWZ, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   }

@@ -46,6 +46,19 @@ __device__ __forceinline__ void lds_group(const uint8_t* p, uint32_t (&w)[B + 1]
   w[B] = 0u;
 }
 
+// A canonical group re-ordered into two streams, codes 0..15 in the low and codes
+// 16..31 in the high halves of its words (one byte permute a word): what the paired
+// layout's expansion takes, which then yields the pairs (i, 16 + i).
+template <int B>
+__device__ __forceinline__ void halves_of(const uint32_t (&w)[B + 1], uint32_t (&z)[B + 1]) {
+#pragma unroll
+  for (int h = 0; h < B; ++h) {
+    const uint32_t sel = ((h & 1) ? 0x0032u : 0x0010u) | (((B + h) & 1) ? 0x7600u : 0x5400u);
+    z[h] = __byte_perm(w[h >> 1], w[(B + h) >> 1], sel);
+  }
+  z[B] = 0u;
+}
+
 // Shift by a compile-time amount, left when positive.
 template <int S>
 __device__ __forceinline__ uint32_t shift(uint32_t v) {
