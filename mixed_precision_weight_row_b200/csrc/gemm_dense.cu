@@ -210,7 +210,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(acc_full(s), 1);
-      ptx::mbar_init(acc_empty(s), 512);     // both CTAs' epilogues
+      ptx::mbar_init(acc_empty(s), 16);      // both CTAs' epilogues, a lane for a warp
     }
     ptx::mbar_init(drain, 1);
     ptx::mbar_fence_init();
@@ -368,7 +368,8 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         }
       }
       ptx::tc_fence_before();
-      ptx::mbar_arrive_cluster(ptx::cluster_addr(acc_empty(u & 1), 0));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(acc_empty(u & 1), 0));
     }
   }
   __syncwarp();

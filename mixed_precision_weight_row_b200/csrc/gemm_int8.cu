@@ -114,10 +114,10 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     }
     for (int s = 0; s < SW; ++s) {
       ptx::mbar_init(full_w(s), 1);
-      ptx::mbar_init(empty_w(s), 128);      // one converter group
+      ptx::mbar_init(empty_w(s), 4);        // one converter group, a lane for a warp
     }
     for (int s = 0; s < SA; ++s) {
-      ptx::mbar_init(full_a(s), 128);       // one converter group
+      ptx::mbar_init(full_a(s), 4);
       ptx::mbar_init(empty_a(s), 1);
     }
     ptx::mbar_init(acc_full, 1);
@@ -212,7 +212,8 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
       }
       w[4 * B] = 0u;
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(empty_w(ws));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(empty_w(ws));
       ok = ptx::mbar_wait(empty_a(sa), ((wb / SA) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitAEmpty));
       if (!ok) break;
       ptx::tc_fence_after();
@@ -233,7 +234,8 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
       }
       ptx::tmem_wait_st();
       ptx::tc_fence_before();
-      ptx::mbar_arrive(full_a(sa));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full_a(sa));
     }
     ptx::grid_dep_wait_then_release();
     // ---------------- epilogue: this warp's rows, a share of the tokens ----------------

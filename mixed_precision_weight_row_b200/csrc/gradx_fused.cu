@@ -125,10 +125,10 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
     }
     for (int s = 0; s < SW; ++s) {
       ptx::mbar_init(full_w(s), 1);
-      ptx::mbar_init(empty_w(s), 128);      // one converter group
+      ptx::mbar_init(empty_w(s), 4);        // one converter group, a lane for a warp
     }
     for (int s = 0; s < SA; ++s) {
-      ptx::mbar_init(full_a(s), 128);       // one converter group
+      ptx::mbar_init(full_a(s), 4);
       ptx::mbar_init(empty_a(s), 1);
     }
     ptx::mbar_init(acc_full, 1);
@@ -237,7 +237,8 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
         for (int i = 0; i < 16; ++i) o[h][i] = dec::scale_pair(v[0][i], s2[h][0], s2[h][1]);
       }
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(empty_w(ws));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(empty_w(ws));
       ok = ptx::mbar_wait(empty_a(sa), ((b / SA) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitAEmpty));
       if (!ok) break;
       uint8_t* a = gsmem + sa * kAStage + (g >> 1) * (BK * 128);
@@ -250,7 +251,8 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
               make_uint4(o[h][4 * j], o[h][4 * j + 1], o[h][4 * j + 2], o[h][4 * j + 3]);
       }
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(full_a(sa));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(full_a(sa));
     }
     // ---------------- epilogue: 32 inputs a warp, a share of the tokens ----------------
     const int quad = warp & 3;                     // tensor-memory lane quadrant
