@@ -51,7 +51,8 @@ struct Code {
   static constexpr uint32_t kXStage = BN * BK;
   static constexpr uint32_t PITCH = 16u * B;
   static constexpr uint32_t kWStage = BM * PITCH;
-  static constexpr int SX = 4;
+  // a stage of xq takes over a microsecond to come: enough of them to cover it
+  static constexpr int SX = BN == 16 ? 16 : (BN == 32 ? 12 : (BN == 64 ? 8 : (BN == 128 ? 6 : 5)));
   static constexpr int SW = BN == 256 ? 4 : 8;
   static constexpr uint32_t kCols = BN <= 32 ? 256 : 512;                 // tensor memory
   static constexpr int SA_all = static_cast<int>((kCols - BN) / kACols);
@@ -64,7 +65,7 @@ struct Code {
     else if constexpr (B == 4) return r * 64u + 16u * (static_cast<uint32_t>(u) ^ ((r >> 1) & 3));
     else return r * PITCH + 16u * u;
   }
-  static constexpr size_t SMEM = SX * kXStage + SW * kWStage + 1024 /*align*/ + 512 /*barriers*/;
+  static constexpr size_t SMEM = SX * kXStage + SW * kWStage + 1024 /*align*/ + 640 /*barriers*/;
   static_assert(SMEM + 1024 <= 232448, "shared memory per block");
   // A stage is always read by the same group: were it another one's turn, that
   // group could find the stage's previous fill, not yet complete, to have the

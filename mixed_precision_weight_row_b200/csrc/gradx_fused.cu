@@ -49,7 +49,9 @@ struct Code {
   static constexpr uint32_t kXStage = BN * BK * 2;
   static constexpr uint32_t PITCH = 16u * B;
   static constexpr uint32_t kWStage = BK * PITCH;
-  static constexpr int SX = BN == 256 ? 3 : 4;
+  // a stage of dy takes over a microsecond to come: enough of them to cover it
+  // (four of 64 tokens bound the kernel to 0.35 us a block)
+  static constexpr int SX = BN == 32 ? 12 : (BN == 64 ? 8 : (BN == 128 ? 6 : 4));
   static constexpr int SW = BN == 256 ? 4 : 8;
   static constexpr uint32_t kCols = BN;                       // tensor memory
   static constexpr CUtensorMapSwizzle WSWZ =
