@@ -45,58 +45,99 @@ __device__ __forceinline__ uint32_t code8(float x, float s) {
 // and a value above 0x7F80 (bf16 infinity) means a NaN was seen.
 __device__ __forceinline__ uint32_t mag2(uint32_t v) { return v & 0x7FFF7FFFu; }
 
-// One CTA per token.  Two passes over the row, the second from L1 / L2.  The
-// next launch may start at once (the decode kernel reads weights before it waits
-// for this one).
-template <bool VEC>
-__global__ void __launch_bounds__(kThreads)
+// Block-wide maximum over T threads.
+template <int T>
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return __reduce_max_sync(0xffffffffu, (threadIdx.x & 31) < T / 32 ? red[threadIdx.x & 31] : 0u);
+}
+
+// Scale of a token whose largest magnitude has the bf16 bits mx; NaN (and codes
+// 0) with an infinity or NaN, so that what is computed from the token is NaN.
+__device__ __forceinline__ float scale8(uint32_t mx) {
+  if (mx >= 0x7F80u) return __uint_as_float(0x7FC00000u);
+  return __fdiv_rn(mx == 0 ? 1.0f : __uint_as_float(mx << 16), 127.0f);
+}
+
+__device__ __forceinline__ uint2 codes8_exact(const uint4& v, float s) {
+  return make_uint2(code8(bf16_lo(v.x), s) | (code8(bf16_hi(v.x), s) << 8) | (code8(bf16_lo(v.y), s) << 16) |
+                        (code8(bf16_hi(v.y), s) << 24),
+                    code8(bf16_lo(v.z), s) | (code8(bf16_hi(v.z), s) << 8) | (code8(bf16_lo(v.w), s) << 16) |
+                        (code8(bf16_hi(v.w), s) << 24));
+}
+
+// The codes of eight values without a division where the nearest whole number is
+// not in doubt: with r = fl32(1 / s), x r and fl32(x / s) are each within 2^-17 of
+// x / s (|x / s| < 128, relative errors of 2^-24), so a whole number that x r is
+// within 1/2 - 2^-14 of is the one nearest to both.  Closer to a tie (about 1 value
+// in 8000) the quotient decides.  Needs a normal 1 / s.
+__device__ __forceinline__ uint2 codes8(const uint4& v, float s, float r) {
+  constexpr float kMagic = 12582912.0f;          // 1.5 * 2^23: adding it rounds to a whole number, in the low bits
+  const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+  float t[8], far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float x = (i & 1) ? bf16_hi(u[i >> 1]) : bf16_lo(u[i >> 1]);
+    t[i] = __fmaf_rn(x, r, kMagic);
+    far = fmaxf(far, fabsf(__fmaf_rn(x, r, -(t[i] - kMagic))));
+  }
+  if (far > 0.5f - 0x1p-14f) return codes8_exact(v, s);
+  uint32_t o[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    o[h] = __byte_perm(__byte_perm(__float_as_uint(t[4 * h]), __float_as_uint(t[4 * h + 1]), 0x0040),
+                       __byte_perm(__float_as_uint(t[4 * h + 2]), __float_as_uint(t[4 * h + 3]), 0x0040), 0x5410);
+  return make_uint2(o[0], o[1]);
+}
+
+// One CTA of T threads per token.  The next launch may start at once (the
+// kernels that follow read weights before they wait for this one).
+// KEEP > 0: rows of whole 16-byte units, of which a thread keeps up to KEEP in
+// registers between the maximum and the codes (one read of x); KEEP = 0: any rows,
+// two passes, the second from L1 / L2.
+template <int T, int KEEP>
+__global__ void __launch_bounds__(T)
 quantize_x_int8_kernel(const uint16_t* __restrict__ x, int K, int stride, uint8_t* __restrict__ xq,
                        float* __restrict__ sx) {
   ptx::grid_dep_wait_then_release();
-  __shared__ uint32_t red[kThreads / 32];
+  __shared__ uint32_t red[T / 32];
   const size_t m = blockIdx.x;
   const uint16_t* row = x + m * static_cast<size_t>(K);
-  uint32_t top = 0;   // two 16-bit maxima
-  if constexpr (VEC) {
-    const uint4* r8 = reinterpret_cast<const uint4*>(row);
-    for (int i = threadIdx.x; i < (K >> 3); i += kThreads) {
-      const uint4 v = __ldg(r8 + i);
-      top = __vmaxu2(top, __vmaxu2(__vmaxu2(mag2(v.x), mag2(v.y)), __vmaxu2(mag2(v.z), mag2(v.w))));
-    }
-  } else {
-    for (int k = threadIdx.x; k < K; k += kThreads) top = __vmaxu2(top, row[k] & 0x7FFFu);
-  }
-  uint32_t mx = max(top & 0xFFFFu, top >> 16);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = mx;
-  __syncthreads();
-  mx = red[0];
-#pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) mx = max(mx, red[i]);
-  const bool finite = mx < 0x7F80u;
-  const float amax = __uint_as_float(mx << 16);
-  // a token with an infinity or NaN: scale NaN, codes 0, so that what is computed from it is NaN
-  const float s = !finite ? __uint_as_float(0x7FC00000u) : __fdiv_rn(mx == 0 ? 1.0f : amax, 127.0f);
-  if (threadIdx.x == 0) sx[m] = s;
   uint8_t* out = xq + m * static_cast<size_t>(stride);
-  if constexpr (VEC) {
+  if constexpr (KEEP > 0) {
     const uint4* r8 = reinterpret_cast<const uint4*>(row);
-    uint2* o8 = reinterpret_cast<uint2*>(out);
-    for (int i = threadIdx.x; i < (stride >> 3); i += kThreads) {
-      uint2 o = make_uint2(0u, 0u);
-      if (finite && i < (K >> 3)) {
-        const uint4 v = __ldg(r8 + i);
-        o.x = code8(bf16_lo(v.x), s) | (code8(bf16_hi(v.x), s) << 8) | (code8(bf16_lo(v.y), s) << 16) |
-              (code8(bf16_hi(v.y), s) << 24);
-        o.y = code8(bf16_lo(v.z), s) | (code8(bf16_hi(v.z), s) << 8) | (code8(bf16_lo(v.w), s) << 16) |
-              (code8(bf16_hi(v.w), s) << 24);
-      }
-      o8[i] = o;
+    uint4 v[KEEP];
+    uint32_t top = 0;   // two 16-bit maxima
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+      const int i = threadIdx.x + j * T;
+      v[j] = i < (K >> 3) ? __ldg(r8 + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j)
+      top = __vmaxu2(top, __vmaxu2(__vmaxu2(mag2(v[j].x), mag2(v[j].y)), __vmaxu2(mag2(v[j].z), mag2(v[j].w))));
+    const uint32_t mx = block_max<T>(max(top & 0xFFFFu, top >> 16), red);
+    const float s = scale8(mx);
+    if (threadIdx.x == 0) sx[m] = s;
+    const bool plain = s > 0x1p-120f;      // 1 / s is far from overflow (false for NaN)
+    const float r = plain ? __fdiv_rn(1.0f, s) : 0.0f;
+#pragma unroll
+    for (int j = 0; j < KEEP; ++j) {
+      const int i = threadIdx.x + j * T;
+      if (i >= (stride >> 3)) continue;      // zeros past K give the zero padding
+      reinterpret_cast<uint2*>(out)[i] =
+          plain ? codes8(v[j], s, r) : (mx < 0x7F80u ? codes8_exact(v[j], s) : make_uint2(0u, 0u));
     }
   } else {
-    for (int k = threadIdx.x; k < stride; k += kThreads)
-      out[k] = finite && k < K ? static_cast<uint8_t>(code8(bf16_val(row[k]), s)) : 0;
+    uint32_t top = 0;
+    for (int k = threadIdx.x; k < K; k += T) top = max(top, row[k] & 0x7FFFu);
+    const uint32_t mx = block_max<T>(top, red);
+    const float s = scale8(mx);
+    if (threadIdx.x == 0) sx[m] = s;
+    for (int k = threadIdx.x; k < stride; k += T)
+      out[k] = mx < 0x7F80u && k < K ? static_cast<uint8_t>(code8(bf16_val(row[k]), s)) : 0;
   }
 }
 
@@ -265,13 +306,24 @@ cudaError_t run_expand_bf16(const uint8_t* packed, const float* scales, int64_t 
 
 cudaError_t launch_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, uint8_t* xq, float* sx,
                                    cudaStream_t stream) {
-  const int stride = static_cast<int>(stride_i8(K));
-  if (K % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0)
-    quantize_x_int8_kernel<true><<<static_cast<unsigned>(M), kThreads, 0, stream>>>(x, static_cast<int>(K), stride,
-                                                                                    xq, sx);
+  const int stride = static_cast<int>(stride_i8(K)), k = static_cast<int>(K);
+  const unsigned grid = static_cast<unsigned>(M);
+  const int units = stride / 8;                    // 16-byte units of x, the padding's included
+  const bool whole = K % 8 == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  // as few threads as hold a row in few registers (one B200, 2048 x 5120: 256 threads
+  // x 3 units 10.0 us, 512 x 2 11.3, 1024 x 1 15.6; 2048 x 17408: 512 x 5 30.7 us, 1024
+  // x 3 44.7), more where a token's latency is what counts (1 x 5120: 512 x 2 3.1 us,
+  // 256 x 3 3.4)
+  if (whole && units <= 256 * 3 && M >= device_info().num_sms)
+    quantize_x_int8_kernel<256, 3><<<grid, 256, 0, stream>>>(x, k, stride, xq, sx);
+  else if (whole && units <= 512 * 2)
+    quantize_x_int8_kernel<512, 2><<<grid, 512, 0, stream>>>(x, k, stride, xq, sx);
+  else if (whole && units <= 512 * 5)
+    quantize_x_int8_kernel<512, 5><<<grid, 512, 0, stream>>>(x, k, stride, xq, sx);
+  else if (whole && units <= 1024 * 8)
+    quantize_x_int8_kernel<1024, 8><<<grid, 1024, 0, stream>>>(x, k, stride, xq, sx);
   else
-    quantize_x_int8_kernel<false><<<static_cast<unsigned>(M), kThreads, 0, stream>>>(x, static_cast<int>(K), stride,
-                                                                                     xq, sx);
+    quantize_x_int8_kernel<256, 0><<<grid, 256, 0, stream>>>(x, k, stride, xq, sx);
   return cudaGetLastError();
 }
 

@@ -97,6 +97,31 @@ def test_quantize_x_int8_exact(mpw, M, K):
     assert _intact(buf, xq.numel(), 0xA5)
 
 
+def test_quantize_x_int8_near_ties(mpw):
+    """Values whose quotient lies on or next to k + 1/2: every bf16 pattern of
+    two binades against several largest values."""
+    torch = _torch()
+    v = (torch.arange(0x3F80, 0x4080, dtype=torch.int32) & 0xFFFF).to(torch.int16).view(torch.bfloat16)
+    rows = []
+    for top in (127.0, 63.5, 254.0, 126.5, 3.0, 255.0, 100.0, 97.0, 120.0, 2.0 ** -100, 2.0 ** 100):
+        big = torch.tensor([top], dtype=torch.bfloat16)
+        for scale in (1.0, -0.25, 16.0):
+            x = (v.float() * scale * (big.float() / 127.0)).to(torch.bfloat16)
+            rows.append(torch.cat([big, x, v, -v])[:1 + 3 * v.numel()])
+    k = torch.arange(-126, 127).float() + 0.5                    # exact ties for a scale of 1
+    n = rows[0].numel()
+    tie = torch.zeros(n, dtype=torch.bfloat16)
+    tie[0], tie[1:1 + k.numel()] = 127.0, k.to(torch.bfloat16)
+    rows.append(tie)
+    x = torch.stack(rows)
+    x = torch.nn.functional.pad(x, (0, -x.shape[1] % 8))
+    codes, sx_ref = oracle.quantize_x_int8(x.float().numpy())
+    for part in (x, x.repeat(200, 1)):                           # either thread count
+        xq, sx = mpw.quantize_x_int8(part.cuda())
+        assert np.array_equal(xq[:len(rows)].cpu().numpy(), oracle.pack_rows_int8(codes))
+        assert np.array_equal(sx[:len(rows)].cpu().numpy().view(np.uint32), sx_ref.view(np.uint32))
+
+
 def test_quantize_x_int8_misaligned_rows(mpw):
     torch = _torch()
     big = _x(1, 1 + 6 * 64, 3).cuda().reshape(-1)
