@@ -113,7 +113,7 @@ mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* p
 size_t mpw_qlinear_grad_x_workspace_bytes(int bits, int layout, int64_t M, int64_t N, int64_t K) {
   if (!bits_ok(bits, kMaxBits) || !layout_ok(layout) || !dims_ok(M, N, K)) return 0;
   if (gradx_fused(bits, M, N, K)) return padded_dy_bytes(M, N);
-  return expanded_bf16_bytes(N, K) + padded_dy_bytes(M, N) + dense_workspace_bytes(M, K, dense_stages(N));
+  return expanded_bf16_bytes(N, K) + padded_dy_bytes(M, N) + dense_workspace_bytes(M, K, N, 1);
 }
 
 mpw_status mpw_qlinear_grad_x(const uint16_t* dy, const uint8_t* packed, const float* scales, int bits, int layout,
@@ -144,9 +144,9 @@ mpw_status mpw_qlinear_grad_x(const uint16_t* dy, const uint8_t* packed, const f
 
 size_t mpw_qlinear_grad_w_int8_workspace_bytes(int dW_type, int64_t M, int64_t N, int64_t K) {
   if ((dW_type != MPW_GRAD_BF16 && dW_type != MPW_GRAD_F32) || !dims_ok(M, N, K)) return 0;
-  const int parts = dW_type == MPW_GRAD_F32 ? 2 : 1;
+  const int parts = dW_type == MPW_GRAD_F32 ? 3 : 1;
   return expanded_bf16_bytes(parts * M, K) + padded_dy_bytes(M, N) +
-         dense_workspace_bytes(N, K, parts * dense_stages(M));
+         dense_workspace_bytes(N, K, M, parts);
 }
 
 mpw_status mpw_qlinear_grad_w_int8(const uint16_t* dy, const uint8_t* xq, const float* sx, int64_t M, int64_t N,
@@ -162,7 +162,7 @@ mpw_status mpw_qlinear_grad_w_int8(const uint16_t* dy, const uint8_t* xq, const 
   if (workspace == nullptr || workspace_bytes < need) return MPW_E_INVALID_ARG;
   if (!aligned(workspace, 16)) return MPW_E_MISALIGNED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  const int parts = f32 ? 2 : 1;
+  const int parts = f32 ? 3 : 1;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   uint16_t* x = reinterpret_cast<uint16_t*>(ws);
   uint8_t* room = ws + expanded_bf16_bytes(parts * M, K);

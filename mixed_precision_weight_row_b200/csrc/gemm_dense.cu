@@ -23,6 +23,13 @@
 // adds the slices of a tile in their order and writes it.  (Letting the slice
 // that arrives last do so cost 40 us where this takes 5: one CTA pair reads what
 // here the whole GPU reads.)
+//
+// The fp32 result of grad_w is meant to hold fp32 accuracy.  Its operand x comes
+// as three bf16 values whose products are summed one after another, the smallest
+// first, and since tensor cores truncate a sum at every step (2048 tokens in one go
+// were off by 1.3e-6 of the result, an fp32 product by 0.8e-6), the sum runs over
+// chunks of 768 tokens that the epilogue adds, rounding to nearest, to the tile in
+// memory (it stays in L2).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>
@@ -56,6 +63,7 @@ struct OpTraits {
   static constexpr bool a_mn = OP == kGradWBf16 || OP == kGradWF32;
   static constexpr bool b_mn = !i8;
   static constexpr int depth = i8 ? 128 : 64;      // steps of r per stage
+  static constexpr int chunk = OP == kGradWF32 ? 12 : 0;    // stages along r per chunk (0: all of them)
 };
 
 template <int BN>
@@ -69,8 +77,8 @@ constexpr uint32_t kPartialWords = BM * kSlicedBN;               // sums of one 
 
 struct Args {
   int64_t I, J;          // results
-  int blocks;            // stages along r per part
-  int parts;             // passes over r, part p reading part p of b
+  int blocks;            // stages along r
+  int parts;             // slices of b (with chunks), each read over all of r
   int whole;             // tiles done in one piece; those behind them in slices
   int slices;
   uint32_t* partial;     // sums of slices: [tile - whole][slice][256 rows x BN]
@@ -90,7 +98,7 @@ struct Args {
 // values (any other rows).
 template <Op OP, int C>
 __device__ __forceinline__ void store_block(const Args& p, int64_t i0, int64_t c0, uint32_t (&v)[C], float rs,
-                                            int lane) {
+                                            bool add, int lane) {
   const int64_t left = p.J - c0, rows = p.I - i0;
   if constexpr (OP == kGradWF32) {
     static_assert(C == 32, "fp32 blocks");
@@ -98,26 +106,41 @@ __device__ __forceinline__ void store_block(const Args& p, int64_t i0, int64_t c
     if (p.vec) {
       transpose_units<8, 4>(v, lane);
       const int q = lane & 7, r0 = lane & ~7;
+      auto unit = [&](int t) { return reinterpret_cast<float4*>(out + (r0 + t) * p.J) + q; };
+      const bool mine = 4 * q < left;
+      if (add) {      // every read before the first write, so that they overlap
+        float4 old[8];
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        if (r0 + t >= rows || 4 * q >= left) continue;
-        float4 o = make_float4(__uint_as_float(v[4 * t]), __uint_as_float(v[4 * t + 1]),
-                               __uint_as_float(v[4 * t + 2]), __uint_as_float(v[4 * t + 3]));
-        float4* dst = reinterpret_cast<float4*>(out + (r0 + t) * p.J) + q;
-        if (p.accumulate) {
-          const float4 old = *dst;
-          o = make_float4(old.x + o.x, old.y + o.y, old.z + o.z, old.w + o.w);
+        for (int t = 0; t < 8; ++t) old[t] = mine && r0 + t < rows ? *unit(t) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          v[4 * t] = __float_as_uint(old[t].x + __uint_as_float(v[4 * t]));
+          v[4 * t + 1] = __float_as_uint(old[t].y + __uint_as_float(v[4 * t + 1]));
+          v[4 * t + 2] = __float_as_uint(old[t].z + __uint_as_float(v[4 * t + 2]));
+          v[4 * t + 3] = __float_as_uint(old[t].w + __uint_as_float(v[4 * t + 3]));
         }
-        *dst = o;
       }
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
+        if (mine && r0 + t < rows)
+          *unit(t) = make_float4(__uint_as_float(v[4 * t]), __uint_as_float(v[4 * t + 1]),
+                                 __uint_as_float(v[4 * t + 2]), __uint_as_float(v[4 * t + 3]));
     } else {
       transpose_units<32, 1>(v, lane);
+float* dst = out + lane;
+      if (add) {
 #pragma unroll
-      for (int t = 0; t < 32; ++t) {
-        if (t >= rows || lane >= left) continue;
-        float* dst = out + t * p.J + lane;
-        *dst = p.accumulate ? *dst + __uint_as_float(v[t]) : __uint_as_float(v[t]);
+        for (int h = 0; h < 32; h += 8) {      // eight rows' reads at a time
+          float old[8];
+#pragma unroll
+          for (int t = 0; t < 8; ++t) old[t] = h + t < rows && lane < left ? dst[(h + t) * p.J] : 0.0f;
+#pragma unroll
+          for (int t = 0; t < 8; ++t) v[h + t] = __float_as_uint(old[t] + __uint_as_float(v[h + t]));
+        }
       }
+#pragma unroll
+      for (int t = 0; t < 32; ++t)
+        if (t < rows && lane < left) dst[t * p.J] = __uint_as_float(v[t]);
     }
   } else {
     if constexpr (OP == kLinearI8) {
@@ -227,17 +250,33 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   const uint32_t tmem = *tmem_slot;
 
   const int tiles = static_cast<int>(((p.I + 2 * BM - 1) / (2 * BM)) * ((p.J + BN - 1) / BN));
-  const int total = p.blocks * p.parts;     // stages per tile
-  // work items: whole tiles, then slices of the others
+  // work items: whole tiles, then slices of the others; an item is a range of
+  // chunks of r, or, of the only one, a range of its stages
   const int items = p.whole + (tiles - p.whole) * p.slices;
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
-  auto stages_of = [&](int it, int& r0, int& r1) {
-    r0 = 0;
-    r1 = total;
+  auto slice_of = [&](int it, int n, int& n0, int& n1) {
+    n0 = 0;
+    n1 = n;
     if (it >= p.whole) {
       const int64_t slice = (it - p.whole) % p.slices;
-      r0 = static_cast<int>(total * slice / p.slices);
-      r1 = static_cast<int>(total * (slice + 1) / p.slices);
+      n0 = static_cast<int>(n * slice / p.slices);
+      n1 = static_cast<int>(n * (slice + 1) / p.slices);
+    }
+  };
+  auto chunks_of = [&](int it, int& c0, int& c1) {
+    c0 = 0;
+    c1 = 1;
+    if constexpr (T::chunk > 0) slice_of(it, (p.blocks + T::chunk - 1) / T::chunk, c0, c1);
+  };
+  // first stage along r and number of stages (all parts) of a chunk of an item
+  auto stages_of = [&](int it, int c, int& rb0, int& n) {
+    if constexpr (T::chunk > 0) {
+      rb0 = c * T::chunk;
+      n = min(T::chunk, p.blocks - rb0) * p.parts;
+    } else {
+      int rb1;
+      slice_of(it, p.blocks, rb0, rb1);
+      n = rb1 - rb0;
     }
   };
   auto place = [&](int it, int64_t& i0, int64_t& j0) {
@@ -253,30 +292,39 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
       uint32_t n = 0;                       // stages filled so far
       for (int it = first; it < items && ok; it += step) {
         int64_t i64, j64;
-        int rb0, rb1;
+        int c0, c1;
         place(it, i64, j64);
-        stages_of(it, rb0, rb1);
+        chunks_of(it, c0, c1);
         const int i0 = static_cast<int>(i64), j0 = static_cast<int>(j64) + static_cast<int>(rank) * (BN / 2);
-        for (int rb = rb0; rb < rb1; ++rb, ++n) {
-          const int s = n % S;
-          ok = ptx::mbar_wait(empty(s), ((n / S) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitXEmpty));
-          if (!ok) break;
-          const int part = rb / p.blocks, r0 = (rb - part * p.blocks) * T::depth;
-          const uint32_t sa = base + s * kStage, sb = sa + kABytes;
-          if (rank == 0) ptx::mbar_arrive_expect_tx(full(s), 2 * kStage);
-          const uint32_t bar = ptx::cluster_addr(full(s), 0);
-          if constexpr (T::a_mn) {
+        for (int ch = c0; ch < c1 && ok; ++ch) {
+          int rb0, stages;
+          stages_of(it, ch, rb0, stages);
+          const int each = T::chunk > 0 ? stages / p.parts : stages;
+          for (int st = 0, pass = 0, in = 0; st < stages; ++st, ++n) {
+            const int s = n % S;
+            ok = ptx::mbar_wait(empty(s), ((n / S) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitXEmpty));
+            if (!ok) break;
+            const int r0 = (rb0 + in) * T::depth, part = p.parts - 1 - pass;
+            if (++in == each) {
+              in = 0;
+              ++pass;
+            }
+            const uint32_t sa = base + s * kStage, sb = sa + kABytes;
+            if (rank == 0) ptx::mbar_arrive_expect_tx(full(s), 2 * kStage);
+            const uint32_t bar = ptx::cluster_addr(full(s), 0);
+            if constexpr (T::a_mn) {
 #pragma unroll
-            for (int c = 0; c < BM / 64; ++c) ptx::tma_load_2d_pair(sa + c * 8192, &tmap_a, bar, i0 + 64 * c, r0);
-          } else {
-            ptx::tma_load_2d_pair(sa, &tmap_a, bar, r0, i0);
-          }
-          if constexpr (T::b_mn) {
+              for (int c = 0; c < BM / 64; ++c) ptx::tma_load_2d_pair(sa + c * 8192, &tmap_a, bar, i0 + 64 * c, r0);
+            } else {
+              ptx::tma_load_2d_pair(sa, &tmap_a, bar, r0, i0);
+            }
+            if constexpr (T::b_mn) {
 #pragma unroll
-            for (int c = 0; c < BN / 128; ++c)
-              ptx::tma_load_3d_pair(sb + c * 8192, &tmap_b, bar, j0 + 64 * c, r0, part);
-          } else {
-            ptx::tma_load_2d_pair(sb, &tmap_b, bar, r0, j0);
+              for (int c = 0; c < BN / 128; ++c)
+                ptx::tma_load_3d_pair(sb + c * 8192, &tmap_b, bar, j0 + 64 * c, r0, part);
+            } else {
+              ptx::tma_load_2d_pair(sb, &tmap_b, bar, r0, j0);
+            }
           }
         }
       }
@@ -295,32 +343,37 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         bool ok = true;
         int s = 0;
         uint32_t phase = 0, u = 0;
-        for (int it = first; it < items && ok; it += step, ++u) {
-          int rb0, rb1;
-          stages_of(it, rb0, rb1);
-          const uint32_t acc = tmem + (u & 1) * 256u;
-          ok = ptx::mbar_wait(acc_empty(u & 1), ((u >> 1) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitAccEmpty));
-          if (!ok) break;
-          ptx::tc_fence_after();
-          for (int rb = rb0; rb < rb1; ++rb) {
-            ok = ptx::mbar_wait(full(s), phase, err, ptx::wait_code(kW, ptx::kWaitFull));
+        for (int it = first; it < items && ok; it += step) {
+          int c0, c1;
+          chunks_of(it, c0, c1);
+          for (int ch = c0; ch < c1; ++ch, ++u) {
+            int rb0, stages;
+            stages_of(it, ch, rb0, stages);
+            const uint32_t acc = tmem + (u & 1) * 256u;
+            ok = ptx::mbar_wait(acc_empty(u & 1), ((u >> 1) & 1) ^ 1, err, ptx::wait_code(kW, ptx::kWaitAccEmpty));
             if (!ok) break;
             ptx::tc_fence_after();
-            const uint32_t sa = base + s * kStage, sb = sa + kABytes;
-            const uint64_t ad = T::a_mn ? ptx::sw128_mnmajor_desc(sa, 8192) : ptx::sw128_kmajor_desc(sa);
-            const uint64_t bd = T::b_mn ? ptx::sw128_mnmajor_desc(sb, 8192) : ptx::sw128_kmajor_desc(sb);
-            // a step is 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major operand
-            constexpr uint64_t da = T::a_mn ? 128 : 2, db = T::b_mn ? 128 : 2;
+            for (int st = 0; st < stages; ++st) {
+              ok = ptx::mbar_wait(full(s), phase, err, ptx::wait_code(kW, ptx::kWaitFull));
+              if (!ok) break;
+              ptx::tc_fence_after();
+              const uint32_t sa = base + s * kStage, sb = sa + kABytes;
+              const uint64_t ad = T::a_mn ? ptx::sw128_mnmajor_desc(sa, 8192) : ptx::sw128_kmajor_desc(sa);
+              const uint64_t bd = T::b_mn ? ptx::sw128_mnmajor_desc(sb, 8192) : ptx::sw128_kmajor_desc(sb);
+              // a step is 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major operand
+              constexpr uint64_t da = T::a_mn ? 128 : 2, db = T::b_mn ? 128 : 2;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              ptx::mma_ss<2, T::i8>(acc, ad + da * k, bd + db * k, idesc, rb != rb0 || k != 0);
-            ptx::mma_commit_pair(empty(s));
-            if (++s == S) {
-              s = 0;
-              phase ^= 1;
+              for (int k = 0; k < 4; ++k)
+                ptx::mma_ss<2, T::i8>(acc, ad + da * k, bd + db * k, idesc, (st | k) != 0);
+              ptx::mma_commit_pair(empty(s));
+              if (++s == S) {
+                s = 0;
+                phase ^= 1;
+              }
             }
+            ptx::mma_commit_pair(acc_full(u & 1));
+            if (!ok) break;
           }
-          ptx::mma_commit_pair(acc_full(u & 1));
         }
         // tensor memory is given back only when no product is under way
         ptx::mma_commit_pair(drain);
@@ -335,41 +388,59 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
     const int quad = warp & 3, half = (warp - kEpiWarp0) >> 2;     // rows, and which blocks of columns
     const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
     uint32_t u = 0;
-    for (int it = first; it < items; it += step, ++u) {
+    bool ok = true;
+    for (int it = first; it < items && ok; it += step) {
       int64_t i0, j0;
+      int c0, c1;
       place(it, i0, j0);
+      chunks_of(it, c0, c1);
       const int64_t iw = i0 + quad * 32;      // the warp's first row
       const float rs = OP == kLinearI8 && iw + lane < p.I ? __ldg(p.row_scale + iw + lane) : 0.0f;
-      if (!ptx::mbar_wait(acc_full(u & 1), (u >> 1) & 1, err, ptx::wait_code(kW, ptx::kWaitAcc))) break;
-      ptx::tc_fence_after();
-      const uint32_t acc = tmem + (u & 1) * 256u + lane_addr;
-      const bool sliced = it >= p.whole;
-      const int tail = it - p.whole;
-      constexpr int C = OP == kGradWF32 ? 32 : 64;      // columns per step
-      const int cols = static_cast<int>(min(static_cast<int64_t>(BN / C), (p.J - j0 + C - 1) / C));
+      for (int ch = c0; ch < c1; ++ch, ++u) {
+        ok = ptx::mbar_wait(acc_full(u & 1), (u >> 1) & 1, err, ptx::wait_code(kW, ptx::kWaitAcc));
+        if (!ok) break;
+        ptx::tc_fence_after();
+        const uint32_t acc = tmem + (u & 1) * 256u + lane_addr;
+        const bool sliced = it >= p.whole;
+        const int tail = it - p.whole;
+        constexpr int C = OP == kGradWF32 ? 32 : 64;      // columns per step
+        const int cols = static_cast<int>(min(static_cast<int64_t>(BN / C), (p.J - j0 + C - 1) / C));
 #pragma unroll 1
-      for (int c = half; c < cols; c += 2) {
-        uint32_t v[C];
+        for (int c = half; c < cols; c += 2) {
+          uint32_t v[C];
 #pragma unroll
-        for (int h = 0; h < C / 32; ++h) ptx::tmem_ld32(acc + C * c + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
+          for (int h = 0; h < C / 32; ++h) ptx::tmem_ld32(acc + C * c + 32 * h, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
 #pragma unroll
-        for (int h = 0; h < C / 32; ++h) ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
-        if (iw >= p.I) continue;
-        if (!sliced) {
-          store_block<OP, C>(p, iw, j0 + C * c, v, rs, lane);
-        } else {
+          for (int h = 0; h < C / 32; ++h) ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
+          if (iw >= p.I) continue;
+          if (!sliced) {
+            store_block<OP, C>(p, iw, j0 + C * c, v, rs, p.accumulate || ch > c0, lane);
+          } else {
 #pragma unroll
-          for (int h = 0; h < C / 32; ++h) {
-            uint4* dst = partial_block(p, tail, static_cast<int>(rank), quad, C / 32 * c + h) + lane;
-            const uint32_t* w = v + 32 * h;
+            for (int h = 0; h < C / 32; ++h) {
+              uint4* dst = partial_block(p, tail, static_cast<int>(rank), quad, C / 32 * c + h) + lane;
+              uint32_t* w = v + 32 * h;
+              if (T::chunk > 0 && ch > c0) {        // this lane's own words of the chunk before
+                uint4 old[8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) dst[32 * q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+                for (int q = 0; q < 8; ++q) old[q] = dst[32 * q];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  const uint32_t x[4] = {old[q].x, old[q].y, old[q].z, old[q].w};
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    w[4 * q + k] = __float_as_uint(__uint_as_float(x[k]) + __uint_as_float(w[4 * q + k]));
+                }
+              }
+#pragma unroll
+              for (int q = 0; q < 8; ++q) dst[32 * q] = make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+            }
           }
         }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(acc_empty(u & 1), 0));
       }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(acc_empty(u & 1), 0));
     }
   }
   __syncwarp();
@@ -413,7 +484,7 @@ dense_join_kernel(const __grid_constant__ Args p) {
       }
     }
   }
-  store_block<OP, 32>(p, i0, j0, v, 0.0f, lane);
+  store_block<OP, 32>(p, i0, j0, v, 0.0f, p.accumulate, lane);
 }
 
 // A K-major operand: rows of `cols` values (dense in r), box of one stage.
@@ -478,12 +549,12 @@ struct Plan {
   int64_t tiles, whole;
   int slices;
 };
-Plan plan_tiles(int64_t I, int64_t J, int64_t stages) {
+Plan plan_tiles(int64_t I, int64_t J, int64_t stages, int64_t most_slices) {
   const int64_t pairs = sm_pairs(), tiles = tile_count(I, J, kSlicedBN), rest = tiles % pairs;
   Plan p{tiles, tiles, 1};
   if (rest == 0) return p;
   double best = static_cast<double>(stages) * 0.38;
-  for (int64_t s = 2; s * rest <= pairs && s * 4 <= stages; ++s) {
+  for (int64_t s = 2; s * rest <= pairs && s <= most_slices; ++s) {
     const double us = static_cast<double>((stages + s - 1) / s) * 0.38 + 10.0;
     if (us < best) {
       best = us;
@@ -492,6 +563,12 @@ Plan plan_tiles(int64_t I, int64_t J, int64_t stages) {
   }
   if (p.slices > 1) p.whole = tiles - rest;
   return p;
+}
+
+// Slices of at least four stages, or (fp32 grad_w, three parts) of whole chunks.
+Plan plan_for(int64_t I, int64_t J, int64_t blocks, int parts) {
+  constexpr int64_t chunk = OpTraits<kGradWF32>::chunk;
+  return plan_tiles(I, J, blocks * parts, parts > 1 ? (blocks + chunk - 1) / chunk : blocks / 4);
 }
 
 template <Op OP, int BN>
@@ -509,7 +586,7 @@ cudaError_t run(const CUtensorMap& a, const CUtensorMap& b, Args p, const Plan& 
 
 template <Op OP>
 cudaError_t run_sliced(const CUtensorMap& a, const CUtensorMap& b, Args p, void* ws, cudaStream_t stream) {
-  const Plan plan = plan_tiles(p.I, p.J, static_cast<int64_t>(p.blocks) * p.parts);
+  const Plan plan = plan_for(p.I, p.J, p.blocks, p.parts);
   p.partial = static_cast<uint32_t*>(ws);
   const cudaError_t e = run<OP, kSlicedBN>(a, b, p, plan, stream);
   if (e != cudaSuccess || plan.slices == 1) return e;
@@ -525,13 +602,11 @@ bool whole16(const void* out, int64_t row_bytes) {
 
 }  // namespace
 
-size_t dense_workspace_bytes(int64_t I, int64_t J, int64_t stages) {
-  const Plan p = plan_tiles(I, J, stages);
+size_t dense_workspace_bytes(int64_t I, int64_t J, int64_t depth, int parts) {
+  const Plan p = plan_for(I, J, (depth + 63) / 64, parts);
   if (p.slices == 1) return 0;
   return static_cast<size_t>(p.tiles - p.whole) * static_cast<size_t>(p.slices) * 2 * kPartialWords * 4;
 }
-
-int64_t dense_stages(int64_t depth) { return (depth + 63) / 64; }
 
 cudaError_t launch_dense_i8(const uint8_t* a, const uint8_t* b, const float* sx, const float* scales, int shift,
                             int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream) {
@@ -567,7 +642,7 @@ cudaError_t launch_dense_grad_x(const uint16_t* dy, const uint16_t* w, int64_t M
   Args p{};
   p.I = M;
   p.J = K;
-  p.blocks = static_cast<int>(dense_stages(N));
+  p.blocks = static_cast<int>((N + 63) / 64);
   p.parts = 1;
   p.out = dx;
   p.vec = whole16(dx, 2 * K);
@@ -581,7 +656,7 @@ cudaError_t launch_dense_grad_w(const uint16_t* dy, const uint16_t* x, int parts
   Args p{};
   p.I = N;
   p.J = K;
-  p.blocks = static_cast<int>(dense_stages(M));
+  p.blocks = static_cast<int>((M + 63) / 64);
   p.parts = parts;
   p.out = dw;
   p.accumulate = accumulate;

@@ -23,8 +23,9 @@ cudaError_t launch_expand_i8(const uint8_t* packed, int64_t N, int64_t K, int bi
 // Packed rows (4..15 bits) -> bf16_rn(s_n * q), rows of stride_bf16(K).
 cudaError_t launch_expand_bf16(const uint8_t* packed, const float* scales, int64_t N, int64_t K, int bits,
                                int layout, uint16_t* out, cudaStream_t stream);
-// 8-bit activations -> bf16 rows of stride_bf16(K): hi = bf16_rn(sx * xq), and,
-// with parts == 2, in the M rows behind, bf16_rn(sx * xq - hi).
+// 8-bit activations -> bf16 rows of stride_bf16(K): bf16_rn(sx * xq), and, with
+// parts == 3, in the M rows behind and the M behind those, what that leaves of
+// fl32(sx * xq), each rounded to bf16: together all of its 24 bits.
 cudaError_t launch_expand_x(const uint8_t* xq, const float* sx, int64_t M, int64_t K, int parts, uint16_t* out,
                             cudaStream_t stream);
 // bf16 [rows, cols] -> the same with rows of stride_bf16(cols).
@@ -54,13 +55,13 @@ cudaError_t launch_gradx_fused(const uint16_t* dy, const uint8_t* packed, const 
 cudaError_t launch_dense_i8(const uint8_t* a, const uint8_t* b, const float* sx, const float* scales, int shift,
                             int64_t M, int64_t N, int64_t K, uint16_t* y, cudaStream_t stream);
 // The gradients take a workspace (dense_workspace_bytes of the result's rows
-// and columns and of the stages of the summed axis; unprepared).
-size_t dense_workspace_bytes(int64_t I, int64_t J, int64_t stages);
-int64_t dense_stages(int64_t depth);
+// and columns, of the length of the summed axis and of the parts of x;
+// unprepared).
+size_t dense_workspace_bytes(int64_t I, int64_t J, int64_t depth, int parts);
 //   dx[m, k] = bf16(sum_n dy[m, n] w[n, k])
 cudaError_t launch_dense_grad_x(const uint16_t* dy, const uint16_t* w, int64_t M, int64_t N, int64_t K, uint16_t* dx,
                                 void* ws, cudaStream_t stream);
-//   dw[n, k] (+)= sum_m dy[m, n] (x[m, k] [+ x[M + m, k] with parts == 2])
+//   dw[n, k] (+)= sum_m dy[m, n] (x[m, k] [+ x[M + m, k] + x[2 M + m, k] with parts == 3])
 cudaError_t launch_dense_grad_w(const uint16_t* dy, const uint16_t* x, int parts, int64_t M, int64_t N, int64_t K,
                                 void* dw, bool f32, bool accumulate, void* ws, cudaStream_t stream);
 

@@ -236,23 +236,25 @@ expand_x_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ sx, in
     const int g = static_cast<int>(idx - m * G);
     const uint2 v = __ldg(reinterpret_cast<const uint2*>(xq + m * xstride) + g);
     const float s = __ldg(sx + m);
-    uint32_t hi[4], lo[4];
+    uint32_t part[PARTS][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t u = i < 2 ? v.x : v.y;
       const int sh = 16 * (i & 1);
-      const float a = s * static_cast<float>(static_cast<int8_t>(u >> sh));
-      const float b = s * static_cast<float>(static_cast<int8_t>(u >> (sh + 8)));
-      const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-      hi[i] = *reinterpret_cast<const uint32_t*>(&h);
-      if constexpr (PARTS == 2) {
-        const __nv_bfloat162 l = __floats2bfloat162_rn(a - bf16_lo(hi[i]), b - bf16_hi(hi[i]));
-        lo[i] = *reinterpret_cast<const uint32_t*>(&l);
+      float a = s * static_cast<float>(static_cast<int8_t>(u >> sh));
+      float b = s * static_cast<float>(static_cast<int8_t>(u >> (sh + 8)));
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        part[p][i] = *reinterpret_cast<const uint32_t*>(&h);
+        a -= bf16_lo(part[p][i]);      // exact
+        b -= bf16_hi(part[p][i]);
       }
     }
-    reinterpret_cast<uint4*>(out + m * stride)[g] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if constexpr (PARTS == 2)
-      reinterpret_cast<uint4*>(out + (M + m) * stride)[g] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+      reinterpret_cast<uint4*>(out + (p * M + m) * stride)[g] =
+          make_uint4(part[p][0], part[p][1], part[p][2], part[p][3]);
   }
 }
 
@@ -362,7 +364,7 @@ cudaError_t launch_expand_x(const uint8_t* xq, const float* sx, int64_t M, int64
                             cudaStream_t stream) {
   const int xstride = static_cast<int>(stride_i8(K)), stride = static_cast<int>(stride_bf16(K));
   const unsigned grid = grid_for(M * (stride / 8));
-  if (parts == 2) expand_x_kernel<2><<<grid, kThreads, 0, stream>>>(xq, sx, M, xstride, stride, out);
+  if (parts == 3) expand_x_kernel<3><<<grid, kThreads, 0, stream>>>(xq, sx, M, xstride, stride, out);
   else expand_x_kernel<1><<<grid, kThreads, 0, stream>>>(xq, sx, M, xstride, stride, out);
   return cudaGetLastError();
 }

@@ -71,11 +71,11 @@ def grad_x_ref(dy, q, s):
 
 def grad_w_ref(dy, codes, sx, fp32: bool):
     """(dW_ref, bound): the activation operand as one bf16 value (bf16
-    result) or as two (fp32 result), fp32 sums."""
+    result) or as three that make up its fp32 value (fp32 result), fp32 sums."""
     x = codes.astype(np.float64) * np.asarray(sx, np.float64)[:, None]
     dy = np.asarray(dy, np.float64)
     dw = dy.T @ x
     mag = np.abs(dy).T @ np.abs(x)
     if fp32:
-        return dw, mag * (U_BF16 ** 2 + (2 * dy.shape[0] + 2) * U_ADD) + 1e-42
+        return dw, mag * (U_BF16 ** 3 + (3 * dy.shape[0] + 2) * U_ADD) + 1e-42
     return dw, mag * (U_BF16 + dy.shape[0] * U_ADD) + np.abs(dw) * U_BF16 + TINY
