@@ -605,9 +605,9 @@ MPW_API mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const ui
  *   dy       device, bf16 [M, N]; 16-byte aligned when N % 8 == 0 (else
  *            MPW_E_MISALIGNED), otherwise natural alignment.
  *   packed, scales, bits (4..15), layout  the linear's rows.
- *   dx       device, bf16 [M, K]: bf16_rn(sum_n dy_mn bf16_rn(s_n q_nk)), the
- *            sum in fp32 (the weight operand of the bf16 tensor cores is
- *            rounded once, at most 2^-8 of its value).
+ *   dx       device, bf16 [M, K]: bf16_rn(sum_n dy_mn w_nk), the sum in fp32,
+ *            w_nk = s_n q_nk rounded to the bf16 of the tensor cores (for b <= 9
+ *            from a value within 2^-16 of it): off by at most 2^-8 of it.
  *   workspace  as for mpw_qlinear_int8, of mpw_qlinear_grad_x_workspace_bytes.
  *
  * mpw_qlinear_grad_w_int8 -- dW = dy^T @ x, x read from its 8-bit checkpoint.
@@ -656,7 +656,10 @@ MPW_API mpw_status mpw_gather_shards(const uint16_t* blocks, int64_t world, int6
  *   other  the first bounded wait (2 s of waiting) inside a TMA / tensor-core
  *          kernel that gave up, as 100 * kernel + place: kernel 1 = per-tile
  *          decode, 2 = tensor-memory decode, 3 = prefill GEMM, 4 = stream-K
- *          decode, 5 = FP8 prefill GEMM, 6 = planned decode pass (mpw_pass_run);
+ *          decode, 5 = FP8 prefill GEMM, 6 = planned decode pass (mpw_pass_run),
+ *          7 = dense products of mpw_qlinear_int8 and the gradients, 8 / 9 =
+ *          mpw_qlinear_int8 on expanding tiles / on streamed rows, 10 =
+ *          mpw_qlinear_grad_x on expanding tiles;
  *          place 1 = x producer waiting for a free stage, 2 = x
  *          producer waiting for its last copies, 3 / 4 = the same for the
  *          weight (or combined) producer, 5 = consumer or MMA issuer waiting
@@ -664,7 +667,9 @@ MPW_API mpw_status mpw_gather_shards(const uint16_t* blocks, int64_t world, int6
  *          7 = converter waiting for a loaded weight stage, 8 = converter
  *          waiting for a free tensor-memory stage, 9 = epilogue waiting for
  *          the accumulator, 10 = sums of squares waiting for a loaded x stage,
- *          11 = a pass item waiting for the linears it depends on.  In the
+ *          11 = a pass item waiting for the linears it depends on, 12 = MMA
+ *          issuer waiting for a free accumulator, 13 = MMA issuer waiting for
+ *          its last products.  In the
  *          planned pass the other waits give up soon after the first one
  *          did (without codes of their own).
  *          The outputs of the call that gave up, and of calls that depend

@@ -515,11 +515,21 @@ def _here(t, name: str) -> int:
     return torch._C._cuda_getDevice()
 
 
-def _scratch(nbytes: int, handle: int, dev: int, workspace):
+def _new(like, shape, dtype, handle: int, dev: int):
+    """A tensor from the allocator of the stream the kernels run on: memory that
+    is still in use on another stream is not handed out, nor this one's to
+    another stream before they are done."""
+    torch = _torch()
+    if handle == torch._C._cuda_getCurrentRawStream(dev):
+        return like.new_empty(shape, dtype=dtype)
+    st = torch.cuda.default_stream(dev) if handle == 0 else torch.cuda.ExternalStream(handle, device=dev)
+    with torch.cuda.stream(st):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _scratch(nbytes: int, like, handle: int, dev: int, workspace):
     """(address, bytes, owner) of the caller's workspace after a check, or of a
-    fresh one: taken from torch's allocator on the stream the kernels run on,
-    so that it is not handed out again before they are done (and belongs to
-    the graph when captured)."""
+    fresh one (which belongs to the graph when captured)."""
     torch = _torch()
     if workspace is not None:
         _arg(workspace, "workspace", torch.uint8, dev, (None,))
@@ -528,11 +538,7 @@ def _scratch(nbytes: int, handle: int, dev: int, workspace):
         return workspace.data_ptr(), workspace.numel(), workspace
     if nbytes == 0:
         return None, 0, None
-    if handle == torch._C._cuda_getCurrentRawStream(dev):
-        ws = torch.empty((nbytes,), dtype=torch.uint8, device="cuda")
-    else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=dev)):
-            ws = torch.empty((nbytes,), dtype=torch.uint8, device="cuda")
+    ws = _new(like, (nbytes,), torch.uint8, handle, dev)
     return ws.data_ptr(), nbytes, ws
 
 
@@ -562,17 +568,16 @@ def quantize_x_int8(x, xq=None, sx=None, stream=None):
     _arg(x, "x", torch.bfloat16, dev, (None, None))
     M, K = x.shape
     rb = _row_bytes8(K)
+    handle = _stream(stream, dev)
     if xq is None:
-        xq = x.new_empty((M, rb), dtype=torch.uint8)
+        xq = _new(x, (M, rb), torch.uint8, handle, dev)
     else:
         _arg(xq, "xq", torch.uint8, dev, (M, rb))
     if sx is None:
-        sx = x.new_empty((M,), dtype=torch.float32)
+        sx = _new(x, (M,), torch.float32, handle, dev)
     else:
         _arg(sx, "sx", torch.float32, dev, (M,))
-    _check(lib.mpw_quantize_x_int8(x.data_ptr(), M, K, xq.data_ptr(), sx.data_ptr(),
-                                 _stream(stream, dev)),
-           "mpw_quantize_x_int8")
+    _check(lib.mpw_quantize_x_int8(x.data_ptr(), M, K, xq.data_ptr(), sx.data_ptr(), handle), "mpw_quantize_x_int8")
     return xq, sx
 
 
@@ -599,13 +604,13 @@ def qlinear_int8(x, packed, scales, bits: int, y=None, layout: str = "canonical"
         M = _arg(xq, "xq", torch.uint8, dev, (None, _row_bytes8(K)))
         _arg(sx, "sx", torch.float32, dev, (M,))
     N = _rows_arg(packed, scales, bits, None, K, dev)
-    if y is None:
-        y = packed.new_empty((M, N), dtype=torch.bfloat16)
-    else:
-        _arg(y, "y", torch.bfloat16, dev, (M, N))
     lay = LAYOUTS[layout]
     handle = _stream(stream, dev)
-    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_int8_workspace_bytes(bits, lay, M, N, K), handle, dev, workspace)
+    if y is None:
+        y = _new(packed, (M, N), torch.bfloat16, handle, dev)
+    else:
+        _arg(y, "y", torch.bfloat16, dev, (M, N))
+    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_int8_workspace_bytes(bits, lay, M, N, K), packed, handle, dev, workspace)
     _check(lib.mpw_qlinear_int8(xq.data_ptr(), sx.data_ptr(), packed.data_ptr(), scales.data_ptr(), bits, lay, M, N, K,
                                 y.data_ptr(), ws, ws_bytes, handle), "mpw_qlinear_int8")
     return y
@@ -621,13 +626,13 @@ def qlinear_grad_x(dy, packed, scales, bits: int, K: int, dx=None, layout: str =
     _arg(dy, "dy", torch.bfloat16, dev, (None, None))
     M, N = dy.shape
     _rows_arg(packed, scales, bits, N, K, dev)
-    if dx is None:
-        dx = dy.new_empty((M, K))
-    else:
-        _arg(dx, "dx", torch.bfloat16, dev, (M, K))
     lay = LAYOUTS[layout]
     handle = _stream(stream, dev)
-    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_grad_x_workspace_bytes(bits, lay, M, N, K), handle, dev, workspace)
+    if dx is None:
+        dx = _new(dy, (M, K), torch.bfloat16, handle, dev)
+    else:
+        _arg(dx, "dx", torch.bfloat16, dev, (M, K))
+    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_grad_x_workspace_bytes(bits, lay, M, N, K), packed, handle, dev, workspace)
     _check(lib.mpw_qlinear_grad_x(dy.data_ptr(), packed.data_ptr(), scales.data_ptr(), bits, lay, M, N, K,
                                   dx.data_ptr(), ws, ws_bytes, handle), "mpw_qlinear_grad_x")
     return dx
@@ -652,13 +657,13 @@ def qlinear_grad_w_int8(dy, xq, sx, K: int, dW=None, dtype=None, accumulate: boo
         raise TypeError("dW must be torch.bfloat16 or torch.float32")
     if accumulate and (dW is None or dtype != torch.float32):
         raise ValueError("accumulate needs a float32 dW")
-    if dW is None:
-        dW = dy.new_empty((N, K), dtype=dtype)
-    else:
-        _arg(dW, "dW", dtype, dev, (N, K))
     kind = GRAD_F32 if dtype == torch.float32 else GRAD_BF16
     handle = _stream(stream, dev)
-    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_grad_w_int8_workspace_bytes(kind, M, N, K), handle, dev, workspace)
+    if dW is None:
+        dW = _new(dy, (N, K), dtype, handle, dev)
+    else:
+        _arg(dW, "dW", dtype, dev, (N, K))
+    ws, ws_bytes, keep = _scratch(lib.mpw_qlinear_grad_w_int8_workspace_bytes(kind, M, N, K), dy, handle, dev, workspace)
     _check(lib.mpw_qlinear_grad_w_int8(dy.data_ptr(), xq.data_ptr(), sx.data_ptr(), M, N, K, dW.data_ptr(), kind,
                                        int(bool(accumulate)), ws, ws_bytes, handle), "mpw_qlinear_grad_w_int8")
     return dW

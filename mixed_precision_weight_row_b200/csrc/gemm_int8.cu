@@ -366,7 +366,7 @@ cudaError_t slices(int64_t M, int64_t N, int64_t K, int* s, double* us) {
   auto kern = gemm_i8_kernel<B, PAIRED, BN>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
-  const ClusterCapacity& cap = cluster_capacity(kern, C::kThreads, C::SMEM);
+  const ClusterCapacity cap = cluster_capacity<gemm_i8_kernel<B, PAIRED, BN>>(C::kThreads, C::SMEM);
   const int64_t tiles = (M + BN - 1) / BN * ((N + BM - 1) / BM), blocks = (K + BK - 1) / BK;
   *s = 1;
   *us = 0.0;

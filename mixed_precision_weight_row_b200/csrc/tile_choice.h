@@ -6,26 +6,30 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "mpw_internal.h"
 
 namespace mpw {
 
 constexpr int kMaxSlices = 4;
 
-// CTAs of the kernel that run at once in clusters of 1 .. kMaxSlices: not every SM
+// CTAs of kernel KERN that run at once in clusters of 1 .. kMaxSlices: not every SM
 // can take part in larger clusters.  Asked of the runtime once per kernel and
-// device (`cache`).
+// device, so that a kernel's choices do not depend on what ran before.
 struct ClusterCapacity {
   int ctas[kMaxSlices + 1] = {};
 };
-template <typename Kernel>
-const ClusterCapacity& cluster_capacity(Kernel kern, int threads, size_t smem) {
+template <auto KERN>
+ClusterCapacity cluster_capacity(int threads, size_t smem) {
   constexpr int kDevices = 64;
+  static std::mutex mutex;
   static ClusterCapacity cache[kDevices];
   const DeviceInfo& d = device_info();
+  std::lock_guard<std::mutex> lock(mutex);
   ClusterCapacity& c = cache[d.device >= 0 && d.device < kDevices ? d.device : 0];
   if (c.ctas[1] == 0) {
-    ClusterCapacity got;
+    c.ctas[1] = d.num_sms;
     for (int s = 2; s <= kMaxSlices; ++s) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(s));
@@ -39,11 +43,11 @@ const ClusterCapacity& cluster_capacity(Kernel kern, int threads, size_t smem) {
       cfg.attrs = attr;
       cfg.numAttrs = 1;
       int n = 0;
-      if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess) got.ctas[s] = n * s < d.num_sms ? n * s : d.num_sms;
-      else (void)cudaGetLastError();
+      if (cudaOccupancyMaxActiveClusters(&n, KERN, &cfg) == cudaSuccess)
+        c.ctas[s] = n * s < d.num_sms ? n * s : d.num_sms;
+      else
+        (void)cudaGetLastError();
     }
-    got.ctas[1] = d.num_sms;
-    c = got;
   }
   return c;
 }

@@ -507,6 +507,32 @@ def test_stream_argument_and_callers_workspace(mpw):
     assert _intact(buf, n, 0xEE)
 
 
+def test_temporaries_of_another_stream_are_not_handed_out(mpw):
+    """Everything a call allocates for a busy side stream stays its own while
+    the current stream allocates and writes the same sizes."""
+    torch = _torch()
+    M, N, K, b = 1100, 264, 512, 6
+    packed, scales = _rows(mpw, _w(N, K, 1), b, "canonical")
+    x, dy = _x(M, K, 0).cuda(), _dy(M, N, 0).cuda()
+    want = _all_ops(mpw, x, dy, packed, scales, b, K)
+    sizes = [(M, mpw.packed_row_bytes(K, 8)), (4 * M,), (N * K,), (6 * M * K,), (2 * M * N,), (4 * N * K,)]
+    st = torch.cuda.Stream()
+    for _ in range(3):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(st):
+            torch.cuda._sleep(20_000_000)
+        y = mpw.qlinear_int8(x, packed, scales, b, stream=st)
+        dx = mpw.qlinear_grad_x(dy, packed, scales, b, K, stream=st)
+        xq, sx = mpw.quantize_x_int8(x, stream=st)
+        dW = mpw.qlinear_grad_w_int8(dy, xq, sx, K, dtype=torch.float32, stream=st)
+        for n in sizes:
+            for _ in range(3):
+                torch.empty(n, dtype=torch.uint8, device="cuda").fill_(0x55)
+        st.synchronize()
+        for a, r in zip((y, dx, dW), want):
+            assert torch.equal(a, r)
+
+
 def test_refusals(mpw):
     torch = _torch()
     M, N, K = 40, 24, 64
