@@ -15,7 +15,13 @@
 // of stages by TMA (128 bytes of r, or 64 steps of r, per stage and operand, in
 // the 128-byte swizzle), one thread of the first CTA issues the products for
 // both into one of two accumulators in tensor memory, and four warps of each
-// write the other one out meanwhile.  Tiles run in groups of kGroup along i,
+// write the other one out meanwhile: bf16 rows of whole, aligned 16-byte units by
+// TMA from a block of 32 rows x 128 bytes per warp in shared memory, others by the
+// lanes, which exchange values for coalesced stores in eight times the
+// instructions (grad_w of 64 x 17408 x 5120, which writes 178 MB: 37 us by TMA, 48
+// by lanes).  fp32 results stay with the lanes, which add to memory as well and
+// leave the ring its last stage: by TMA 16 x 5120 x 17408 took 77 us against 81,
+// but 256 x 4096 x 4096 39 against 33 and 1000 x 4096 x 4096 107 against 87.  Tiles run in groups of kGroup along i,
 // so that the CTAs working at one time share operand rows in L2.
 //
 // Tiles that do not fill a last round of the SM pairs are cut into slices of r
@@ -66,11 +72,14 @@ struct OpTraits {
   static constexpr int chunk = OP == kGradWF32 ? 12 : 0;    // stages along r per chunk (0: all of them)
 };
 
-template <int BN>
+constexpr uint32_t kOutBlock = 32 * 128;        // 32 rows x 128 bytes of a result, per epilogue warp
+
+template <Op OP, int BN>
 struct Tile {
   static constexpr uint32_t kStage = kABytes + BN / 2 * 128;     // half of the pair's rows of b
-  static constexpr int S = static_cast<int>((232448 - 1024 /*align*/ - 256 /*barriers*/) / kStage);
-  static constexpr size_t kSmem = S * kStage + 1024 + 256;
+  static constexpr uint32_t kOutBytes = OP == kGradWF32 ? 0 : 8 * kOutBlock;
+  static constexpr int S = static_cast<int>((232448 - 1024 /*align*/ - kOutBytes - 256 /*barriers*/) / kStage);
+  static constexpr size_t kSmem = S * kStage + 1024 + kOutBytes + 256;
 };
 constexpr int kSlicedBN = 256;                                   // the width of tiles that may be sliced
 constexpr uint32_t kPartialWords = BM * kSlicedBN;               // sums of one CTA's half of a tile
@@ -87,8 +96,54 @@ struct Args {
   const float* col_scale;
   int shift;
   bool accumulate;
-  bool vec;              // rows of out are whole, aligned 16-byte units
+  bool vec;              // rows of out are whole, aligned 16-byte units (tmap_out is then valid)
 };
+
+// C columns of a row, scaled (int8 linear) and rounded to bf16, as pairs.
+template <Op OP, int C>
+__device__ __forceinline__ void bf16_pairs(const Args& p, int64_t c0, uint32_t (&v)[C], float rs, int lane,
+                                           uint32_t (&o)[C / 2]) {
+  if constexpr (OP == kLinearI8) {
+    const int64_t left = p.J - c0;
+#pragma unroll
+    for (int h = 0; h < C / 32; ++h) {
+      const float mine = 32 * h + lane < left ? __ldg(p.col_scale + c0 + 32 * h + lane) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        const float cs = __shfl_sync(0xffffffffu, mine, c);
+        uint32_t& d = v[32 * h + c];
+        d = __float_as_uint(static_cast<float>(static_cast<int32_t>(d) >> p.shift) * cs * rs);
+      }
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C / 2; ++c) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
+    o[c] = *reinterpret_cast<const uint32_t*>(&r);
+  }
+}
+
+// Writes 64 columns c0 .. c0 + 63 of the 32 bf16 rows i0 .. i0 + 31, of which this
+// lane holds row i0 + lane, by TMA from `block` (this warp's 4 KB of shared memory,
+// in the 128-byte swizzle).
+template <Op OP>
+__device__ __forceinline__ void store_block_tma(const Args& p, const void* tmap, uint8_t* block, int64_t i0, int64_t c0,
+                                                uint32_t (&v)[64], float rs, int lane) {
+  uint32_t o[32];
+  bf16_pairs<OP, 64>(p, c0, v, rs, lane, o);
+  if (lane == 0) ptx::bulk_wait_read();      // the block's last store has read it
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<uint4*>(block + lane * 128 + 16 * (q ^ (lane & 7))) =
+        make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+  ptx::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    ptx::tma_store_2d(tmap, ptx::smem_addr(block), static_cast<int32_t>(c0), static_cast<int32_t>(i0));
+    ptx::bulk_commit();
+  }
+}
 
 // Writes C columns c0 .. c0 + C - 1 of the 32 result rows i0 .. i0 + 31, of which
 // this lane holds row i0 + lane (C = 32, or 64 for bf16: 128 bytes of a row
@@ -143,24 +198,8 @@ float* dst = out + lane;
         if (t < rows && lane < left) dst[t * p.J] = __uint_as_float(v[t]);
     }
   } else {
-    if constexpr (OP == kLinearI8) {
-#pragma unroll
-      for (int h = 0; h < C / 32; ++h) {
-        const float mine = 32 * h + lane < left ? __ldg(p.col_scale + c0 + 32 * h + lane) : 0.0f;
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float cs = __shfl_sync(0xffffffffu, mine, c);
-          uint32_t& d = v[32 * h + c];
-          d = __float_as_uint(static_cast<float>(static_cast<int32_t>(d) >> p.shift) * cs * rs);
-        }
-      }
-    }
-    uint32_t o[C / 2];      // pairs of columns
-#pragma unroll
-    for (int c = 0; c < C / 2; ++c) {
-      const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1]));
-      o[c] = *reinterpret_cast<const uint32_t*>(&r);
-    }
+    uint32_t o[C / 2];
+    bf16_pairs<OP, C>(p, c0, v, rs, lane, o);
     uint16_t* out = static_cast<uint16_t*>(p.out) + i0 * p.J + c0;
     if (p.vec) {
       constexpr int U = C / 8;
@@ -206,16 +245,17 @@ __device__ __forceinline__ uint4* partial_block(const Args& p, int64_t item, int
 template <Op OP, int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__ CUtensorMap tmap_b,
-             const __grid_constant__ Args p, int32_t* err) {
+             const __grid_constant__ CUtensorMap tmap_out, const __grid_constant__ Args p, int32_t* err) {
   using T = OpTraits<OP>;
   static_assert(!T::b_mn || BN % 128 == 0, "whole chunks of an MN-major b per CTA");
-  constexpr uint32_t kStage = Tile<BN>::kStage;
-  constexpr int S = Tile<BN>::S;
+  constexpr uint32_t kStage = Tile<OP, BN>::kStage;
+  constexpr int S = Tile<OP, BN>::S;
   constexpr int32_t kW = ptx::kWaitDense;
   extern __shared__ uint8_t dsmem_raw[];
   const uint32_t raw = ptx::smem_addr(dsmem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;       // 1024-aligned for the 128-byte swizzle
-  uint64_t* bars = reinterpret_cast<uint64_t*>(dsmem_raw + (base - raw) + S * kStage);
+  uint8_t* out_blocks = dsmem_raw + (base - raw) + S * kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(out_blocks + Tile<OP, BN>::kOutBytes);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * S + 5);
   const uint32_t bar0 = ptx::smem_addr(bars);
   auto full = [&](int s) { return bar0 + 8u * s; };
@@ -413,7 +453,10 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
 #pragma unroll
           for (int h = 0; h < C / 32; ++h) ptx::tmem_wait_ld(*reinterpret_cast<uint32_t(*)[32]>(v + 32 * h));
           if (iw >= p.I) continue;
-          if (!sliced) {
+          if (OP != kGradWF32 && !sliced && p.vec) {
+            if constexpr (OP != kGradWF32)
+              store_block_tma<OP>(p, &tmap_out, out_blocks + (warp - kEpiWarp0) * kOutBlock, iw, j0 + C * c, v, rs, lane);
+          } else if (!sliced) {
             store_block<OP, C>(p, iw, j0 + C * c, v, rs, p.accumulate || ch > c0, lane);
           } else {
 #pragma unroll
@@ -442,6 +485,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
         if (lane == 0) ptx::mbar_arrive_cluster(ptx::cluster_addr(acc_empty(u & 1), 0));
       }
     }
+    if (lane == 0) ptx::bulk_wait();
   }
   __syncwarp();
   ptx::tc_fence_before();
@@ -565,6 +609,22 @@ Plan plan_tiles(int64_t I, int64_t J, int64_t stages, int64_t most_slices) {
   return p;
 }
 
+// The result, rows of `cols` values, for stores of 32 rows x 128 bytes; false (and
+// no map) when its rows are not whole, aligned 16-byte units.
+bool map_out(CUtensorMap* m, void* out, bool f32, int64_t rows, int64_t cols) {
+  const int64_t row_bytes = cols * (f32 ? 4 : 2);
+  if (row_bytes % 16 != 0 || reinterpret_cast<uintptr_t>(out) % 16 != 0) return false;
+  auto encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+  const cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box,
+                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Slices of at least four stages, or (fp32 grad_w, three parts) of whole chunks.
 Plan plan_for(int64_t I, int64_t J, int64_t blocks, int parts) {
   constexpr int64_t chunk = OpTraits<kGradWF32>::chunk;
@@ -573,14 +633,16 @@ Plan plan_for(int64_t I, int64_t J, int64_t blocks, int parts) {
 
 template <Op OP, int BN>
 cudaError_t run(const CUtensorMap& a, const CUtensorMap& b, Args p, const Plan& plan, cudaStream_t stream) {
+  CUtensorMap out = a;      // unused unless p.vec
+  p.vec = map_out(&out, p.out, OP == kGradWF32, p.I, p.J);
   auto kern = dense_kernel<OP, BN>;
-  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Tile<BN>::kSmem);
+  const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Tile<OP, BN>::kSmem);
   if (e != cudaSuccess) return e;
   p.whole = static_cast<int>(plan.whole);
   p.slices = plan.slices;
   const int64_t items = plan.whole + (plan.tiles - plan.whole) * plan.slices, pairs = sm_pairs();
-  kern<<<static_cast<unsigned>(2 * (items < pairs ? items : pairs)), kThreads, Tile<BN>::kSmem, stream>>>(
-      a, b, p, device_error_word());
+  kern<<<static_cast<unsigned>(2 * (items < pairs ? items : pairs)), kThreads, Tile<OP, BN>::kSmem, stream>>>(
+      a, b, out, p, device_error_word());
   return cudaGetLastError();
 }
 
@@ -590,14 +652,12 @@ cudaError_t run_sliced(const CUtensorMap& a, const CUtensorMap& b, Args p, void*
   p.partial = static_cast<uint32_t*>(ws);
   const cudaError_t e = run<OP, kSlicedBN>(a, b, p, plan, stream);
   if (e != cudaSuccess || plan.slices == 1) return e;
+  CUtensorMap unused;
+  p.vec = map_out(&unused, p.out, OP == kGradWF32, p.I, p.J);
   p.whole = static_cast<int>(plan.whole);
   p.slices = plan.slices;
   dense_join_kernel<OP><<<static_cast<unsigned>((plan.tiles - plan.whole) * kJoinBlocks), kJoinThreads, 0, stream>>>(p);
   return cudaGetLastError();
-}
-
-bool whole16(const void* out, int64_t row_bytes) {
-  return row_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
 }
 
 }  // namespace
@@ -624,7 +684,6 @@ cudaError_t launch_dense_i8(const uint8_t* a, const uint8_t* b, const float* sx,
   p.row_scale = sx;
   p.col_scale = scales;
   p.shift = shift;
-  p.vec = whole16(y, 2 * N);
   const int64_t tiles = tile_count(M, N, bn);
   const Plan plan{tiles, tiles, 1};
   switch (bn) {
@@ -645,7 +704,6 @@ cudaError_t launch_dense_grad_x(const uint16_t* dy, const uint16_t* w, int64_t M
   p.blocks = static_cast<int>((N + 63) / 64);
   p.parts = 1;
   p.out = dx;
-  p.vec = whole16(dx, 2 * K);
   return run_sliced<kGradX>(ma, mb, p, ws, stream);
 }
 
@@ -660,7 +718,6 @@ cudaError_t launch_dense_grad_w(const uint16_t* dy, const uint16_t* x, int parts
   p.parts = parts;
   p.out = dw;
   p.accumulate = accumulate;
-  p.vec = whole16(dw, (f32 ? 4 : 2) * K);
   return f32 ? run_sliced<kGradWF32>(ma, mb, p, ws, stream) : run_sliced<kGradWBf16>(ma, mb, p, ws, stream);
 }
 
