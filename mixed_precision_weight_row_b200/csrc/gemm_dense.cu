@@ -9,20 +9,21 @@
 // No operand is transposed in memory: tcgen05 reads either order from shared
 // memory, and every result is written row by row as the caller wants it.
 //
-// Two CTAs on neighbouring SMs (cta_group::2) compute tiles of 256 x BN
-// results, each holding 128 rows of a, half of b's rows and its own 128 rows of
-// the result; one CTA per SM walks over the tiles.  Warp 0 of each fills a ring
-// of stages by TMA (128 bytes of r, or 64 steps of r, per stage and operand, in
-// the 128-byte swizzle), one thread of the first CTA issues the products for
-// both into one of two accumulators in tensor memory, and four warps of each
-// write the other one out meanwhile: bf16 rows of whole, aligned 16-byte units by
-// TMA from a block of 32 rows x 128 bytes per warp in shared memory, others by the
+// Two CTAs on neighbouring SMs (cta_group::2) compute tiles of 256 x BN results,
+// each holding 128 rows of a, half of b's rows and its own 128 rows of the
+// result; one CTA per SM walks over the tiles.  Warp 0 of each fills a ring of
+// stages by TMA (128 bytes of r, or 64 steps of r, per stage and operand, in the
+// 128-byte swizzle), one thread of the first CTA issues the products for both
+// into one of two accumulators in tensor memory, and four warps of each write
+// the other one out meanwhile: bf16 rows of whole, aligned 16-byte units by TMA
+// from a block of 32 rows x 128 bytes per warp in shared memory, others by the
 // lanes, which exchange values for coalesced stores in eight times the
-// instructions (grad_w of 64 x 17408 x 5120, which writes 178 MB: 37 us by TMA, 48
-// by lanes).  fp32 results stay with the lanes, which add to memory as well and
-// leave the ring its last stage: by TMA 16 x 5120 x 17408 took 77 us against 81,
-// but 256 x 4096 x 4096 39 against 33 and 1000 x 4096 x 4096 107 against 87.  Tiles run in groups of kGroup along i,
-// so that the CTAs working at one time share operand rows in L2.
+// instructions (grad_w of 64 x 17408 x 5120, which writes 178 MB: 37 us by TMA,
+// 48 by lanes).  fp32 results stay with the lanes, which add to memory as well
+// and leave the ring its last stage: by TMA 16 x 5120 x 17408 took 77 us against
+// 81, but 256 x 4096 x 4096 39 against 33 and 1000 x 4096 x 4096 107 against 87.
+// Tiles run in groups of kGroup along i, so that the CTAs working at one time
+// share operand rows in L2.
 //
 // Tiles that do not fill a last round of the SM pairs are cut into slices of r
 // for all of them: a slice leaves its sums in a workspace, and a second kernel
@@ -96,7 +97,7 @@ struct Args {
   const float* col_scale;
   int shift;
   bool accumulate;
-  bool vec;              // rows of out are whole, aligned 16-byte units (tmap_out is then valid)
+  bool vec;              // rows of out are whole, aligned 16-byte units (tmap_out is then valid for bf16)
 };
 
 // C columns of a row, scaled (int8 linear) and rounded to bf16, as pairs.
@@ -182,7 +183,7 @@ __device__ __forceinline__ void store_block(const Args& p, int64_t i0, int64_t c
                                  __uint_as_float(v[4 * t + 2]), __uint_as_float(v[4 * t + 3]));
     } else {
       transpose_units<32, 1>(v, lane);
-float* dst = out + lane;
+      float* dst = out + lane;
       if (add) {
 #pragma unroll
         for (int h = 0; h < 32; h += 8) {      // eight rows' reads at a time
@@ -609,19 +610,20 @@ Plan plan_tiles(int64_t I, int64_t J, int64_t stages, int64_t most_slices) {
   return p;
 }
 
-// The result, rows of `cols` values, for stores of 32 rows x 128 bytes; false (and
-// no map) when its rows are not whole, aligned 16-byte units.
-bool map_out(CUtensorMap* m, void* out, bool f32, int64_t rows, int64_t cols) {
-  const int64_t row_bytes = cols * (f32 ? 4 : 2);
-  if (row_bytes % 16 != 0 || reinterpret_cast<uintptr_t>(out) % 16 != 0) return false;
+bool whole_units(const void* out, int64_t row_bytes) {
+  return row_bytes % 16 == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0;
+}
+
+// The bf16 result, for stores of 32 rows x 128 bytes.
+bool map_out(CUtensorMap* m, void* out, int64_t rows, int64_t cols) {
   auto encode = tensor_map_encoder();
   if (encode == nullptr) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
-  const cuuint32_t box[2] = {f32 ? 32u : 64u, 32};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+  const cuuint32_t box[2] = {64, 32};
   const cuuint32_t estr[2] = {1, 1};
-  return encode(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box,
-                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, out, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -633,8 +635,9 @@ Plan plan_for(int64_t I, int64_t J, int64_t blocks, int parts) {
 
 template <Op OP, int BN>
 cudaError_t run(const CUtensorMap& a, const CUtensorMap& b, Args p, const Plan& plan, cudaStream_t stream) {
-  CUtensorMap out = a;      // unused unless p.vec
-  p.vec = map_out(&out, p.out, OP == kGradWF32, p.I, p.J);
+  CUtensorMap out = a;      // unused unless rows are written by TMA
+  p.vec = whole_units(p.out, p.J * (OP == kGradWF32 ? 4 : 2));
+  if (OP != kGradWF32 && p.vec && !map_out(&out, p.out, p.I, p.J)) return cudaErrorInvalidValue;
   auto kern = dense_kernel<OP, BN>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), Tile<OP, BN>::kSmem);
   if (e != cudaSuccess) return e;
@@ -652,8 +655,7 @@ cudaError_t run_sliced(const CUtensorMap& a, const CUtensorMap& b, Args p, void*
   p.partial = static_cast<uint32_t*>(ws);
   const cudaError_t e = run<OP, kSlicedBN>(a, b, p, plan, stream);
   if (e != cudaSuccess || plan.slices == 1) return e;
-  CUtensorMap unused;
-  p.vec = map_out(&unused, p.out, OP == kGradWF32, p.I, p.J);
+  p.vec = whole_units(p.out, p.J * (OP == kGradWF32 ? 4 : 2));
   p.whole = static_cast<int>(plan.whole);
   p.slices = plan.slices;
   dense_join_kernel<OP><<<static_cast<unsigned>((plan.tiles - plan.whole) * kJoinBlocks), kJoinThreads, 0, stream>>>(p);

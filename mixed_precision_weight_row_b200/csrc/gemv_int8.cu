@@ -125,7 +125,17 @@ gemv_i8_kernel(const __grid_constant__ Args p, int32_t* err) {
         for (int t = 0; t < MT; ++t) acc[r][t] = 0;
       }
     }
-    if (!ptx::mbar_wait(bar0 + 8u * slot, phase, err, ptx::wait_code(kW, ptx::kWaitWFull))) break;
+    if (!ptx::mbar_wait(bar0 + 8u * slot, phase, err, ptx::wait_code(kW, ptx::kWaitWFull))) {
+      // nothing may still be landing in shared memory when the CTA exits
+      for (int j = i + 1; j < min(i + p.slots, steps); ++j) {
+        if (++slot == p.slots) {
+          slot = 0;
+          phase ^= 1;
+        }
+        ptx::mbar_wait(bar0 + 8u * slot, phase, err, ptx::wait_code(kW, ptx::kWaitWTail));
+      }
+      break;
+    }
     const uint8_t* w0 = ring + static_cast<uint32_t>(slot * R) * seg_bytes;
     const int g0 = seg * (p.seg_codes >> 5), g1 = min(G, g0 + (p.seg_codes >> 5));
 #pragma unroll 1
