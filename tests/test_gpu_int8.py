@@ -5,6 +5,7 @@ fp64 definitions (oracle/int8.py), with the bounds derived there.
   for odd K, misaligned rows, zero, tiny, infinite and NaN tokens.
 * mpw_qlinear_int8: every width and layout from one token to several tiles,
   ragged M, N and K, the largest sums, full prefill shapes on sampled rows.
+* rows, tokens and results whose offsets pass 32 bits.
 * gradients: every width, both result types, accumulation, odd sizes, the
   differences of the product.
 * together: a two-layer step with gradients, accumulated weight gradients to
@@ -248,6 +249,56 @@ def test_qlinear_int8_workload_sampled(mpw, name, M, b):
     assert mpw.device_error() == 0
 
 
+@pytest.mark.parametrize("M", [1, 20, 1100])
+def test_qlinear_int8_rows_past_32_bits(mpw, M):
+    """2.4 GB of rows, 4.8 G codes: a block of rows again and again, so that every block's results are the same."""
+    torch = _torch()
+    rows, times, K, b = 4096, 72, 16384, 4
+    block, scales = mpw.quantize_pack(workloads.gen_weight_torch(rows, K, 0.02, 5), b)
+    xq, sx = mpw.quantize_x_int8(workloads.gen_x(M, K, 6).cuda())
+    ref = mpw.qlinear_int8(None, block, scales, b, xq=xq, sx=sx, K=K)
+    y = mpw.qlinear_int8(None, block.repeat(times, 1), scales.repeat(times), b, xq=xq, sx=sx, K=K)
+    assert torch.equal(y.view(M, times, rows), ref[:, None].expand(-1, times, -1))
+    assert mpw.device_error() == 0
+
+
+def test_tokens_past_32_bits(mpw):
+    """4.9 G activations, then 4.4 G results and their gradients: tokens again
+    and again.  Of dy only the last token, or the last column, is not zero:
+    every sum is one product, whatever the order."""
+    torch = _torch()
+    tokens, times, K = 1000, 300, 16384
+    x = workloads.gen_x(tokens, K, 7).cuda()
+    xq, sx = mpw.quantize_x_int8(x)
+    xq2, sx2 = mpw.quantize_x_int8(x.repeat(times, 1))
+    assert torch.equal(sx2.view(times, tokens), sx.expand(times, -1))
+    for t in range(times):
+        assert torch.equal(xq2[t * tokens:(t + 1) * tokens], xq)
+    del x, xq2, sx2
+
+    times, N, K, b = 110, 40000, 64, 6
+    M = tokens * times
+    packed, scales = mpw.quantize_pack(workloads.gen_weight_torch(N, K, 0.02, 8), b)
+    xq, sx = mpw.quantize_x_int8(workloads.gen_x(tokens, K, 9).cuda())
+    xq2, sx2 = xq.repeat(times, 1), sx.repeat(times)
+    ref = mpw.qlinear_int8(None, packed, scales, b, xq=xq, sx=sx, K=K)
+    y = mpw.qlinear_int8(None, packed, scales, b, xq=xq2, sx=sx2, K=K)
+    for t in range(times):
+        assert torch.equal(y[t * tokens:(t + 1) * tokens], ref)
+    dy = y.zero_()
+    dy[:, -1] = torch.arange(M, device="cuda") % 251 - 125
+    dx = mpw.qlinear_grad_x(dy, packed, scales, b, K)
+    one = mpw.qlinear_grad_x(dy[:1000, -8:].contiguous(), packed[-8:], scales[-8:], b, K)
+    assert torch.equal(dx[:1000], one)
+    assert torch.equal(dx[-1000:], mpw.qlinear_grad_x(dy[-1000:, -8:].contiguous(), packed[-8:], scales[-8:], b, K))
+    dy.zero_()
+    dy[-1] = torch.arange(N, device="cuda") % 241 - 120
+    for dt in (torch.bfloat16, torch.float32):
+        dW = mpw.qlinear_grad_w_int8(dy, xq2, sx2, K, dtype=dt)
+        assert torch.equal(dW, mpw.qlinear_grad_w_int8(dy[-1:], xq2[-1:], sx2[-1:], K, dtype=dt))
+    assert mpw.device_error() == 0
+
+
 # ---- gradients --------------------------------------------------------------
 
 
@@ -330,6 +381,34 @@ def test_grad_w_many_tokens_and_one(mpw, M, N, K, fp32):
 @pytest.mark.parametrize("M,N,K", [(16, 64, 128), (130, 257, 333), (300, 130, 1280), (4100, 300, 500)])
 def test_grad_w_accumulates(mpw, M, N, K):
     _check_grad_w(mpw, M, N, K, True, accumulate=True)
+
+
+@pytest.mark.parametrize("M", [20, 800])
+def test_grad_x_rows_past_32_bits(mpw, M):
+    """4.8 G codes (9.7 GB of them expanded): of dy only the last column is not zero."""
+    torch = _torch()
+    rows, times, K, b = 4096, 72, 16384, 4
+    block, scales = mpw.quantize_pack(workloads.gen_weight_torch(rows, K, 0.02, 5), b)
+    dy = torch.zeros((M, rows * times), dtype=torch.bfloat16, device="cuda")
+    dy[:, -1] = _dy(M, 1, 3).cuda()[:, 0]
+    dx = mpw.qlinear_grad_x(dy, block.repeat(times, 1), scales.repeat(times), b, K)
+    assert torch.equal(dx, mpw.qlinear_grad_x(dy[:, -8:].contiguous(), block[-8:], scales[-8:], b, K))
+    assert mpw.device_error() == 0
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+def test_grad_w_results_past_32_bits(mpw, fp32):
+    """4.8 G results, a block of rows again and again; one token: sums of one product."""
+    torch = _torch()
+    rows, times, K = 4096, 72, 16384
+    dt = torch.float32 if fp32 else torch.bfloat16
+    xq, sx = mpw.quantize_x_int8(workloads.gen_x(1, K, 4).cuda())
+    dy = _dy(1, rows, 5).cuda()
+    ref = mpw.qlinear_grad_w_int8(dy, xq, sx, K, dtype=dt)
+    dW = mpw.qlinear_grad_w_int8(dy.repeat(1, times), xq, sx, K, dtype=dt)
+    for t in range(times):
+        assert torch.equal(dW[t * rows:(t + 1) * rows], ref)
+    assert mpw.device_error() == 0
 
 
 def test_gradients_are_the_differences_of_the_product(mpw):
