@@ -92,8 +92,9 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, float s, float r) {
   return make_uint2(o[0], o[1]);
 }
 
-// One CTA of T threads per token.  The next launch may start at once (the
-// kernels that follow read weights before they wait for this one).
+// One CTA of T threads per token.  It never lets the next launch start ahead of
+// its end: its results are packed rows and scales, which the kernels that take
+// rows read before they wait.
 // KEEP > 0: rows of whole 16-byte units, of which a thread keeps up to KEEP in
 // registers between the maximum and the codes (one read of x); KEEP = 0: any rows,
 // two passes, the second from L1 / L2.
@@ -101,7 +102,6 @@ template <int T, int KEEP>
 __global__ void __launch_bounds__(T)
 quantize_x_int8_kernel(const uint16_t* __restrict__ x, int K, int stride, uint8_t* __restrict__ xq,
                        float* __restrict__ sx) {
-  ptx::grid_dep_wait_then_release();
   __shared__ uint32_t red[T / 32];
   const size_t m = blockIdx.x;
   const uint16_t* row = x + m * static_cast<size_t>(K);

@@ -560,6 +560,33 @@ def test_two_streams_at_once(mpw, M):
                 assert torch.equal(a, r)
 
 
+@pytest.mark.parametrize("M", [1, 40, 300, 900])
+def test_rows_quantized_by_the_call_before(mpw, M):
+    """Quantized activations are packed rows: a product that follows them at once reads the new ones."""
+    torch = _torch()
+    N, K = 20000, 2048
+    xq, sx = mpw.quantize_x_int8(workloads.gen_x(M, K, 1).cuda())
+    dy = _dy(M, N, 2).cuda()
+    keys = [workloads.gen_x(N, K, 3 + i).cuda() for i in range(3)]
+    rows = torch.empty((N, K), dtype=torch.uint8, device="cuda")
+    scales = torch.empty((N,), dtype=torch.float32, device="cuda")
+
+    def both(wait):
+        out = []
+        for op in (lambda: mpw.qlinear_int8(None, rows, scales, 8, xq=xq, sx=sx, K=K),
+                   lambda: mpw.qlinear_grad_x(dy, rows, scales, 8, K)):
+            for key in keys:
+                mpw.quantize_x_int8(key, xq=rows, sx=scales)
+                if wait:
+                    torch.cuda.synchronize()
+                out.append(op())
+        return out
+
+    for _ in range(3):
+        for got, want in zip(both(False), both(True)):
+            assert torch.equal(got, want)
+
+
 def test_stream_argument_and_callers_workspace(mpw):
     torch = _torch()
     M, N, K, b = 1050, 264, 512, 7
