@@ -289,6 +289,7 @@ dense_kernel(const __grid_constant__ CUtensorMap tmap_a, const __grid_constant__
   ptx::cluster_sync();     // barriers and tensor memory of both CTAs are ready
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  ptx::grid_dep_wait_then_release();
 
   const int tiles = static_cast<int>(((p.I + 2 * BM - 1) / (2 * BM)) * ((p.J + BN - 1) / BN));
   // work items: whole tiles, then slices of the others; an item is a range of
@@ -504,6 +505,7 @@ constexpr int kJoinBlocks = 2 * 4 * (kSlicedBN / 32) * 32 / kJoinThreads;     //
 template <Op OP>
 __global__ void __launch_bounds__(kJoinThreads)
 dense_join_kernel(const __grid_constant__ Args p) {
+  ptx::grid_dep_wait_then_release();
   constexpr int BN = kSlicedBN;
   const int lane = threadIdx.x & 31;
   const int tail = static_cast<int>(blockIdx.x) / kJoinBlocks;
@@ -644,9 +646,8 @@ cudaError_t run(const CUtensorMap& a, const CUtensorMap& b, Args p, const Plan& 
   p.whole = static_cast<int>(plan.whole);
   p.slices = plan.slices;
   const int64_t items = plan.whole + (plan.tiles - plan.whole) * plan.slices, pairs = sm_pairs();
-  kern<<<static_cast<unsigned>(2 * (items < pairs ? items : pairs)), kThreads, Tile<OP, BN>::kSmem, stream>>>(
-      a, b, out, p, device_error_word());
-  return cudaGetLastError();
+  return launch_behind(kern, static_cast<unsigned>(2 * (items < pairs ? items : pairs)), kThreads, Tile<OP, BN>::kSmem,
+                       stream, a, b, out, p, device_error_word());
 }
 
 template <Op OP>
@@ -658,8 +659,8 @@ cudaError_t run_sliced(const CUtensorMap& a, const CUtensorMap& b, Args p, void*
   p.vec = whole_units(p.out, p.J * (OP == kGradWF32 ? 4 : 2));
   p.whole = static_cast<int>(plan.whole);
   p.slices = plan.slices;
-  dense_join_kernel<OP><<<static_cast<unsigned>((plan.tiles - plan.whole) * kJoinBlocks), kJoinThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_behind(dense_join_kernel<OP>, static_cast<unsigned>((plan.tiles - plan.whole) * kJoinBlocks),
+                       kJoinThreads, 0, stream, p);
 }
 
 }  // namespace

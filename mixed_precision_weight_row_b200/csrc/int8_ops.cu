@@ -178,6 +178,7 @@ template <int B, bool PAIRED>
 __global__ void __launch_bounds__(kThreads)
 expand_i8_kernel(const uint32_t* __restrict__ packed, int64_t N, int G, int rw, int stride,
                  uint8_t* __restrict__ out) {
+  ptx::grid_dep_wait_then_release();
   const int64_t total = N * G;
   const int lane = threadIdx.x & 31;
   for (int64_t w0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane; w0 < total;
@@ -196,6 +197,7 @@ __global__ void __launch_bounds__(kThreads)
 expand_bf16_kernel(const uint32_t* __restrict__ packed, const float* __restrict__ scales, int64_t N, int G, int rw,
                    int stride, uint16_t* __restrict__ out) {
   constexpr int P = dec::GemmParts<B>::parts;
+  ptx::grid_dep_wait_then_release();
   const int64_t total = N * G;
   const int lane = threadIdx.x & 31;
   for (int64_t w0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane; w0 < total;
@@ -228,6 +230,7 @@ template <int PARTS>
 __global__ void __launch_bounds__(kThreads)
 expand_x_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ sx, int64_t M, int xstride, int stride,
                 uint16_t* __restrict__ out) {
+  ptx::grid_dep_wait_then_release();
   const int G = stride >> 3;
   const int64_t total = M * G;
   for (int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; idx < total;
@@ -260,6 +263,7 @@ expand_x_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ sx, in
 
 __global__ void __launch_bounds__(kThreads)
 pad_bf16_kernel(const uint16_t* __restrict__ in, int64_t rows, int cols, int stride, uint16_t* __restrict__ out) {
+  ptx::grid_dep_wait_then_release();
   const int G = stride >> 3;
   const int64_t total = rows * G;
   for (int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; idx < total;
@@ -285,10 +289,8 @@ cudaError_t run_expand_i8(const uint8_t* packed, int64_t N, int64_t K, int layou
   const int stride = static_cast<int>(stride_i8(K));
   const uint32_t* src = reinterpret_cast<const uint32_t*>(packed);
   if (layout == kLayoutPaired)
-    expand_i8_kernel<B, true><<<grid_for(N * G), kThreads, 0, stream>>>(src, N, G, rw, stride, out);
-  else
-    expand_i8_kernel<B, false><<<grid_for(N * G), kThreads, 0, stream>>>(src, N, G, rw, stride, out);
-  return cudaGetLastError();
+    return launch_behind(expand_i8_kernel<B, true>, grid_for(N * G), kThreads, 0, stream, src, N, G, rw, stride, out);
+  return launch_behind(expand_i8_kernel<B, false>, grid_for(N * G), kThreads, 0, stream, src, N, G, rw, stride, out);
 }
 
 template <int B>
@@ -298,10 +300,10 @@ cudaError_t run_expand_bf16(const uint8_t* packed, const float* scales, int64_t 
   const int stride = static_cast<int>(stride_bf16(K));
   const uint32_t* src = reinterpret_cast<const uint32_t*>(packed);
   if (layout == kLayoutPaired)
-    expand_bf16_kernel<B, true><<<grid_for(N * G), kThreads, 0, stream>>>(src, scales, N, G, rw, stride, out);
-  else
-    expand_bf16_kernel<B, false><<<grid_for(N * G), kThreads, 0, stream>>>(src, scales, N, G, rw, stride, out);
-  return cudaGetLastError();
+    return launch_behind(expand_bf16_kernel<B, true>, grid_for(N * G), kThreads, 0, stream, src, scales, N, G, rw,
+                         stride, out);
+  return launch_behind(expand_bf16_kernel<B, false>, grid_for(N * G), kThreads, 0, stream, src, scales, N, G, rw,
+                       stride, out);
 }
 
 }  // namespace
@@ -364,16 +366,14 @@ cudaError_t launch_expand_x(const uint8_t* xq, const float* sx, int64_t M, int64
                             cudaStream_t stream) {
   const int xstride = static_cast<int>(stride_i8(K)), stride = static_cast<int>(stride_bf16(K));
   const unsigned grid = grid_for(M * (stride / 8));
-  if (parts == 3) expand_x_kernel<3><<<grid, kThreads, 0, stream>>>(xq, sx, M, xstride, stride, out);
-  else expand_x_kernel<1><<<grid, kThreads, 0, stream>>>(xq, sx, M, xstride, stride, out);
-  return cudaGetLastError();
+  auto kern = parts == 3 ? expand_x_kernel<3> : expand_x_kernel<1>;
+  return launch_behind(kern, grid, kThreads, 0, stream, xq, sx, M, xstride, stride, out);
 }
 
 cudaError_t launch_pad_bf16(const uint16_t* in, int64_t rows, int64_t cols, uint16_t* out, cudaStream_t stream) {
   const int stride = static_cast<int>(stride_bf16(cols));
-  pad_bf16_kernel<<<grid_for(rows * (stride / 8)), kThreads, 0, stream>>>(in, rows, static_cast<int>(cols), stride,
-                                                                        out);
-  return cudaGetLastError();
+  return launch_behind(pad_bf16_kernel, grid_for(rows * (stride / 8)), kThreads, 0, stream, in, rows,
+                       static_cast<int>(cols), stride, out);
 }
 
 }  // namespace mpw
