@@ -52,8 +52,8 @@ struct Code {
   static constexpr uint32_t PITCH = 16u * B;
   static constexpr uint32_t kWStage = BM * PITCH;
   // a stage of xq takes over a microsecond to come: enough of them to cover it
-  static constexpr int SX = BN == 16 ? 16 : (BN == 32 ? 12 : (BN == 64 ? 8 : (BN == 128 ? 6 : 5)));
-  static constexpr int SW = BN == 256 ? 4 : 8;
+  static constexpr int SX = BN == 16 ? 16 : (BN == 32 ? 12 : (BN == 64 ? 8 : (BN < 256 ? 6 : 5)));
+  static constexpr int SW = BN >= 192 ? 4 : 8;
   static constexpr uint32_t kCols = BN <= 32 ? 256 : 512;                 // tensor memory
   static constexpr int SA_all = static_cast<int>((kCols - BN) / kACols);
   static constexpr int SA = SA_all > 8 ? 8 : SA_all;
@@ -355,59 +355,57 @@ cudaError_t run(const uint8_t* xq, const float* sx, const uint8_t* packed, const
                             static_cast<int>((K + BK - 1) / BK), splits, device_error_word());
 }
 
-// Slices for tiles of BN tokens and the time they promise.  (One B200, a block 0.29 us
-// with up to 128 tokens and 0.42 us with 256; for instance 4096 x 4096, b = 4, 256
-// tokens: 128-token tiles 10.9 us, 256 in four slices 13.0, 256 whole 15.8; 1024 x
-// 5120, b = 5, 128 tokens: tiles of 64 in four slices 6.9, 128 in four 7.9, 128 whole
-// 14.1.)
+// A tile width, its slices and the time they promise.
+struct Choice {
+  int bn = 0, slices = 1;
+  double us = 0.0;
+};
+
+// Takes tiles of BN tokens when they promise 7% less than the wider ones before
+// them (narrow tiles read more).  (One B200, a block 0.29 us with up to 128 tokens,
+// 0.36 us with 192 and 0.42 us with 256; for instance 4096 x 4096, b = 4, 256 tokens:
+// 128-token tiles 10.9 us, 256 in four slices 13.0, 256 whole 15.8; 1024 x 5120,
+// b = 5, 128 tokens: tiles of 64 in four slices 6.9, 128 in four 7.9, 128 whole
+// 14.1; 17408 x 5120, b = 7, 300 tokens: 192 41.7, 256 44.0.)
 template <int B, bool PAIRED, int BN>
-cudaError_t slices(int64_t M, int64_t N, int64_t K, int* s, double* us) {
+cudaError_t consider(int64_t M, int64_t N, int64_t K, Choice* best) {
   using C = Code<B, BN>;
   auto kern = gemm_i8_kernel<B, PAIRED, BN>;
   const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void*>(kern), C::SMEM);
   if (e != cudaSuccess) return e;
   const ClusterCapacity cap = cluster_capacity<gemm_i8_kernel<B, PAIRED, BN>>(C::kThreads, C::SMEM);
   const int64_t tiles = (M + BN - 1) / BN * ((N + BM - 1) / BM), blocks = (K + BK - 1) / BK;
-  *s = 1;
-  *us = 0.0;
+  Choice c;
   for (int i = 1; i <= kMaxSlices && (i == 1 || i * 4 <= blocks); ++i) {
     if (cap.ctas[i] == 0) continue;
-    const double t = tile_time(tiles * i, cap.ctas[i], blocks, i, BN, BN == 256 ? 0.42 : 0.29, 1.7);
-    if (*us == 0.0 || t < 0.95 * *us) {
-      *us = t;
-      *s = i;
-    }
+    const double block = BN == 256 ? 0.42 : (BN == 192 ? 0.36 : 0.29);
+    const double t = tile_time(tiles * i, cap.ctas[i], blocks, i, BN, block, 1.7);
+    if (c.bn == 0 || t < 0.95 * c.us) c = Choice{BN, i, t};
   }
+  if (best->bn == 0 || c.us < 0.93 * best->us) *best = c;
   return cudaSuccess;
 }
 
-// The widest tile that M fills, or one or two halvings of it where those promise
-// 7% less (they read more).
-template <int B, bool PAIRED, int BN, int HALVINGS>
-cudaError_t run_tile(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int64_t M,
+// The widest tile that M fills, or a narrower one.
+template <int B, bool PAIRED, int... BN>
+cudaError_t run_best(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int64_t M,
                      int64_t N, int64_t K, uint16_t* y, cudaStream_t stream) {
-  int s = 1;
-  double us = 0.0;
-  const cudaError_t e = slices<B, PAIRED, BN>(M, N, K, &s, &us);
+  Choice best;
+  cudaError_t e = cudaSuccess;
+  ((e = e == cudaSuccess ? consider<B, PAIRED, BN>(M, N, K, &best) : e), ...);
   if (e != cudaSuccess) return e;
-  if constexpr (HALVINGS > 0 && BN > 16) {
-    int s2 = 1;
-    double us2 = 0.0;
-    const cudaError_t e2 = slices<B, PAIRED, BN / 2>(M, N, K, &s2, &us2);
-    if (e2 != cudaSuccess) return e2;
-    if (us2 < 0.93 * us) return run_tile<B, PAIRED, BN / 2, HALVINGS - 1>(xq, sx, packed, scales, M, N, K, y, stream);
-  }
-  return run<B, PAIRED, BN>(xq, sx, packed, scales, M, N, K, y, s, stream);
+  ((e = best.bn == BN ? run<B, PAIRED, BN>(xq, sx, packed, scales, M, N, K, y, best.slices, stream) : e), ...);
+  return e;
 }
 
 template <int B, bool PAIRED>
 cudaError_t run_bn(const uint8_t* xq, const float* sx, const uint8_t* packed, const float* scales, int64_t M,
                    int64_t N, int64_t K, uint16_t* y, cudaStream_t stream) {
-  if (M <= 16) return run_tile<B, PAIRED, 16, 0>(xq, sx, packed, scales, M, N, K, y, stream);
-  if (M <= 32) return run_tile<B, PAIRED, 32, 1>(xq, sx, packed, scales, M, N, K, y, stream);
-  if (M <= 64) return run_tile<B, PAIRED, 64, 2>(xq, sx, packed, scales, M, N, K, y, stream);
-  if (M <= 128) return run_tile<B, PAIRED, 128, 2>(xq, sx, packed, scales, M, N, K, y, stream);
-  return run_tile<B, PAIRED, 256, 2>(xq, sx, packed, scales, M, N, K, y, stream);
+  if (M <= 16) return run_best<B, PAIRED, 16>(xq, sx, packed, scales, M, N, K, y, stream);
+  if (M <= 32) return run_best<B, PAIRED, 32, 16>(xq, sx, packed, scales, M, N, K, y, stream);
+  if (M <= 64) return run_best<B, PAIRED, 64, 32, 16>(xq, sx, packed, scales, M, N, K, y, stream);
+  if (M <= 128) return run_best<B, PAIRED, 128, 64, 32>(xq, sx, packed, scales, M, N, K, y, stream);
+  return run_best<B, PAIRED, 256, 192, 128, 64>(xq, sx, packed, scales, M, N, K, y, stream);
 }
 
 template <int B>
