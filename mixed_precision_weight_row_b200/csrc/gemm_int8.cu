@@ -44,9 +44,11 @@ template <int B, int BN>
 struct Code {
   // groups of four converter warps: with many tokens a block's products take
   // long enough for four groups to pay (17408 x 5120, b = 6, 256 tokens: 27.2 to
-  // 24.8 us), with few the threads' start costs more than it gives (4096 x 4096,
-  // b = 4, 32 tokens: 7.0 against 8.6 us)
-  static constexpr int G = BN >= 128 ? 4 : 2;
+  // 24.8 us), and with 64 for the widths whose codes cross bytes, which take the
+  // most operations (5120 x 17408, b = 6: 22.8 to 21.0; b = 4: 16.8, 17.1); with few
+  // the threads' start costs more than it gives (4096 x 4096, 32 tokens, b = 4: 7.7
+  // against 8.7, b = 6: 8.9 against 9.4)
+  static constexpr int G = BN >= 128 || (BN == 64 && B > 4 && B < 8) ? 4 : 2;
   static constexpr int kThreads = (kConvWarp0 + 4 * G) * 32;
   static constexpr uint32_t kXStage = BN * BK;
   static constexpr uint32_t PITCH = 16u * B;
