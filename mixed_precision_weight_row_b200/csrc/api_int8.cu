@@ -31,16 +31,17 @@ bool rows_are_bytes(int bits, int layout) { return bits == 8 && layout == MPW_LA
 // How a call of the int8 linear runs: a few tokens on the kernel that streams
 // packed rows, up to a thousand on the one that expands them on the way to the
 // tensor cores, more on expanded rows (the only one that takes a workspace).
-// One B200, us: 5120 x 6144, b = 6: 4 tokens 9.6 / 10.7 (first / second), 8
-// tokens 15.6 / 10.9; 5120 x 17408, b = 5: 2 tokens 14.7 / 22.6, 4 tokens 26.8
-// / 22.9; 17408 x 5120, b = 8: 4 tokens 20.1 / 17.5.  17408 x 5120, b = 6: 512
-// tokens 45 / 67 (second / third), 1024 tokens 86 / 88, 2048 tokens 168 / 141.
-// Rows that already are bytes need no expansion: 5120 x 6144, b = 8: 256
-// tokens 15.7 / 17.2, 512 tokens 22.2 / 19.0.
+// One B200, us: 5120 x 6144, b = 6: 4 tokens 9.6 / 10.4 (first / second), 8
+// tokens 15.6 / 10.4; 5120 x 17408, b = 5: 2 tokens 14.7 / 19.5, 4 tokens 26.8
+// / 19.5; 17408 x 5120, b = 8: 4 tokens 20.1 / 17.3.  b = 6, second / third: 512
+// tokens 17408 x 5120 45 / 60, 5120 x 6144 22 / 26; 1024 tokens 86 / 84, 42 / 36,
+// 4096 x 4096 18 / 21; 1280 tokens 107 / 96, 43 / 36, 33 / 25.  Rows that already
+// are bytes need no expansion: 5120 x 6144, b = 8: 128 tokens 12.3 / 13.4, 256
+// tokens 16.2 / 13.8, 512 tokens 20.2 / 17.6.
 enum class Int8Path { kGemv, kFused, kDense };
 Int8Path int8_path(int bits, int layout, int64_t M, int64_t N, int64_t K) {
   if ((M <= 2 || (M <= 4 && K <= 8192 && bits <= 7)) && gemv_i8_fits(bits, M, K)) return Int8Path::kGemv;
-  if (M <= (rows_are_bytes(bits, layout) ? 256 : 1024) && gemm_i8_fits(M, N)) return Int8Path::kFused;
+  if (M <= (rows_are_bytes(bits, layout) ? 192 : 1024) && gemm_i8_fits(M, N)) return Int8Path::kFused;
   return Int8Path::kDense;
 }
 
@@ -65,8 +66,8 @@ mpw_status padded_dy(const uint16_t** dy, int64_t M, int64_t N, uint8_t* room, c
 }
 
 // How grad_x runs: rows expanded on the way to the tensor cores, or first.  One
-// B200, us, 17408 x 5120, b = 6: 48 tokens 40 / 88, 512 tokens 95 / 132, 1024
-// tokens 189 / 168; 5120 x 17408, b = 7, 1024 tokens: 165 / 177.
+// B200, us, b = 6: 256 tokens 17408 x 5120 47 / 90, 4096 x 4096 18 / 26; 768 tokens
+// 112 / 138, 31 / 33, 5120 x 6144 41 / 47; 1024 tokens 174 / 165, 32 / 33, 71 / 63.
 bool gradx_fused(int bits, int64_t M, int64_t N, int64_t K) { return M <= 768 && gradx_fused_fits(bits, M, N, K); }
 
 }  // namespace
