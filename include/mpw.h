@@ -561,7 +561,8 @@ MPW_API mpw_status mpw_qlinear_fp8(const uint8_t* xq, const float* sx, const uin
  * xq is stored as canonical 8-bit packed rows (row stride 16 * ceil(K / 16) =
  * mpw_packed_row_bytes(K, 8), zero padding), so (xq, sx) is at once the
  * operand of the product, an 8-bit checkpoint of x for the backward pass
- * (mpw_qlinear_grad_w_int8), and something mpw_unpack and mpw_dequantize read.
+ * (mpw_qlinear_grad_w_int8), something mpw_unpack and mpw_dequantize read, and
+ * packed rows (b = 8) with their scales for a product with other activations.
  *
  * mpw_quantize_x_int8 -- x bf16 [M, K] -> xq rows and sx fp32 [M].
  *   xq  device, uint8 [M, mpw_packed_row_bytes(K, 8)], 16-byte aligned.
