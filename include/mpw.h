@@ -608,7 +608,8 @@ MPW_API mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const ui
  *   packed, scales, bits (4..15), layout  the linear's rows.
  *   dx       device, bf16 [M, K]: bf16_rn(sum_n dy_mn w_nk), the sum in fp32,
  *            w_nk = s_n q_nk rounded to the bf16 of the tensor cores (for b <= 9
- *            from a value within 2^-16 of it): off by at most 2^-8 of it.
+ *            from a value within 2^-16 of it): off by at most 2^-8 of it, or by
+ *            2^-134 (half of bf16's smallest step) where that is more.
  *   workspace  as for mpw_qlinear_int8, of mpw_qlinear_grad_x_workspace_bytes.
  *
  * mpw_qlinear_grad_w_int8 -- dW = dy^T @ x, x read from its 8-bit checkpoint.

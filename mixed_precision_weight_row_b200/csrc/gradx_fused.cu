@@ -214,10 +214,10 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
     float next[2] = {scale_of(wg, 0), scale_of(wg, 1)};     // read a turn ahead
     for (int b = wg; b < nbs; b += kGroups) {
       const int ws = b % SW, sa = b % SA;
-      uint32_t s2[2][2];                           // the rows' scales as pairs of bf16, high and low part
+      dec::PairScale s2[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        dec::split_scale(next[h], s2[h][0], s2[h][1]);
+        s2[h] = dec::split_scale<B>(next[h]);
         next[h] = scale_of(b + kGroups, h);
       }
       ok = ptx::mbar_wait(full_w(ws), (b / SW) & 1, err, ptx::wait_code(kW, ptx::kWaitWFull));
@@ -226,17 +226,15 @@ gradx_kernel(const __grid_constant__ CUtensorMap tmap_dy, const __grid_constant_
       uint32_t o[2][16];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t w[B + 1], v[dec::GemmParts<B>::parts][16];
+        uint32_t w[B + 1];
         C::load(stage, r0 + 32 * h, g, w);
         if constexpr (PAIRED) {
-          dec::gemm_expand_group<B, true>(w, v);
+          dec::scaled_group<B, true>(w, s2[h], o[h]);
         } else {
           uint32_t z[B + 1];
           i8::halves_of<B>(w, z);
-          dec::gemm_expand_group<B, true>(z, v);
+          dec::scaled_group<B, true>(z, s2[h], o[h]);
         }
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[h][i] = dec::scale_pair(v[0][i], s2[h][0], s2[h][1]);
       }
       ptx::fence_proxy_async_smem();
       __syncwarp();

@@ -196,24 +196,22 @@ template <int B, bool PAIRED>
 __global__ void __launch_bounds__(kThreads)
 expand_bf16_kernel(const uint32_t* __restrict__ packed, const float* __restrict__ scales, int64_t N, int G, int rw,
                    int stride, uint16_t* __restrict__ out) {
-  constexpr int P = dec::GemmParts<B>::parts;
   ptx::grid_dep_wait_then_release();
   const int64_t total = N * G;
   const int lane = threadIdx.x & 31;
   for (int64_t w0 = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x - lane; w0 < total;
        w0 += static_cast<int64_t>(gridDim.x) * kThreads) {
     const Group e(w0 + lane, total, G);
-    uint32_t w[B + 1] = {}, v[P][16], o[16];
+    uint32_t w[B + 1] = {}, o[16];
     if (e.in) load_group<B>(packed + e.n * rw, e.g, rw, w);
-    dec::gemm_expand_group<B, PAIRED>(w, v);
     const float s = e.in ? __ldg(scales + e.n) : 0.0f;
-    uint32_t hi, lo;
-    dec::split_scale(s, hi, lo);
+    if constexpr (B <= 9) {
+      dec::scaled_group<B, PAIRED>(w, dec::split_scale<B>(s), o);
+    } else {
+      uint32_t v[2][16];
+      dec::gemm_expand_group<B, PAIRED>(w, v);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      if constexpr (P == 1) {
-        o[i] = dec::scale_pair(v[0][i], hi, lo);
-      } else {
+      for (int i = 0; i < 16; ++i) {
         // the parts' sum is exact in fp32: the code has at most 15 bits
         const __nv_bfloat162 r = __floats2bfloat162_rn((bf16_lo(v[0][i]) + bf16_lo(v[1][i])) * s,
                                                        (bf16_hi(v[0][i]) + bf16_hi(v[1][i])) * s);

@@ -1,0 +1,94 @@
+"""The int8 linear and the gradients at the ends of the number range and of
+their arguments: scales far from one."""
+import numpy as np
+import pytest
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+
+U_SUB = 2.0 ** -134           # half of bf16's smallest step
+
+
+@pytest.fixture(scope="module")
+def mpw():
+    import mixed_precision_weight_row_b200 as m
+
+    return m
+
+
+def _torch():
+    import torch
+
+    return torch
+
+
+def _w(N, K, seed):
+    return np.random.default_rng(seed).standard_normal((N, K)).astype(np.float32) * np.float32(0.02)
+
+
+def _rows(mpw, W, b, layout="canonical"):
+    torch = _torch()
+    packed, scales = mpw.quantize_pack(torch.from_numpy(W).cuda(), b)
+    if layout != "canonical":
+        packed = mpw.repack(packed, W.shape[1], b, "canonical", layout)
+    return packed, scales
+
+
+def _inside(got, ref, bound, what):
+    got = got.double().cpu().numpy()
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} out of bound, first at {np.argwhere(bad)[:3].tolist()}"
+
+
+# ---- scales -----------------------------------------------------------------
+
+TINY_SCALES = [4e-41, 6e-40, 1e-39, 7e-39, 1.2e-38, 3e-38, 1e-37, 1e-36, 1e-35, 1e-33]
+
+
+@pytest.mark.parametrize("layout", ["canonical", "paired"])
+@pytest.mark.parametrize("M", [40, 300, 800])
+@pytest.mark.parametrize("b", [4, 6, 8, 9, 12])
+def test_grad_x_tiny_scales(mpw, b, M, layout):
+    """A weight operand w = s q is off by at most half a step of bf16: 2^-8 of
+    it, or 2^-134 below bf16's normal numbers."""
+    torch = _torch()
+    N, K = 70, 96
+    W = _w(N, K, b)
+    packed, _ = _rows(mpw, W, b, layout)
+    q, _ = oracle.quantize(W, b)
+    s = np.array([TINY_SCALES[n % len(TINY_SCALES)] for n in range(N)], np.float32)
+    dy = (torch.randn((M, N), generator=torch.Generator().manual_seed(M)) * 1e34).to(torch.bfloat16)
+    # rows of very different scales, each alone against its own bound
+    for part in range(len(TINY_SCALES)):
+        d = torch.zeros_like(dy)
+        d[:, part::len(TINY_SCALES)] = dy[:, part::len(TINY_SCALES)]
+        dx = mpw.qlinear_grad_x(d.cuda(), packed, torch.from_numpy(s).cuda(), b, K, layout=layout)
+        ref, bound = oracle.grad_x_ref(d.float().numpy(), q, s)
+        bound = bound + (np.abs(d.double().numpy()).sum(1) * U_SUB)[:, None]
+        _inside(dx, ref, bound, f"b={b} {layout} M={M} s={TINY_SCALES[part]}")
+
+
+@pytest.mark.parametrize("M", [40, 800])
+@pytest.mark.parametrize("b", [4, 6, 8, 9, 12])
+def test_grad_x_largest_scales(mpw, b, M):
+    """Zero codes stay zeros under the largest finite scales, and codes whose
+    product with them is finite keep it."""
+    torch = _torch()
+    N, K = 24, 64
+    W = _w(N, K, b)
+    W[3] = 0
+    W[7] = 0
+    packed, scales = _rows(mpw, W, b)
+    dy = (torch.randn((M, N), generator=torch.Generator().manual_seed(M)) * 1e-3).to(torch.bfloat16).cuda()
+    want = mpw.qlinear_grad_x(dy, packed, scales, b, K)
+    scales[3], scales[7] = 3.4028234e38, 3.395e38
+    assert torch.equal(mpw.qlinear_grad_x(dy, packed, scales, b, K), want)
+    q, s = oracle.quantize(W, b)
+    s = s.copy()
+    s[5] = np.float32(3e38 / 2 ** (b - 1))
+    scales[3], scales[7], scales[5] = 1.0, 1.0, float(s[5])
+    dy = dy * 1e-3
+    dx = mpw.qlinear_grad_x(dy, packed, scales, b, K)
+    ref, bound = oracle.grad_x_ref(dy.float().cpu().numpy(), q, s)
+    _inside(dx, ref, bound, f"b={b} M={M}")
