@@ -617,8 +617,11 @@ MPW_API mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const ui
  *   xq, sx   from mpw_quantize_x_int8 of the forward pass's x [M, K].
  *   dW_type  MPW_GRAD_BF16: dW bf16 [N, K], the operand sx_m xq_mk rounded to
  *            bf16, fp32 sums.  MPW_GRAD_F32: dW fp32 [N, K], the operand as a
- *            sum of three bf16 values (all 24 bits of fl32(sx_m xq_mk)), fp32
- *            sums; three products, so about a third of the speed.
+ *            sum of three bf16 values (all 24 bits of fl32(sx_m xq_mk), in steps
+ *            of 2^-133), fp32 sums; three products, so about a third of the
+ *            speed.  With either, an infinite dy_mn gives dW_nk the infinity of
+ *            its product with the operand, NaN where xq_mk is 0 (MPW_GRAD_F32:
+ *            and where |sx_m xq_mk| is below 2^-124).
  *   accumulate  nonzero (MPW_GRAD_F32 only, else MPW_E_INVALID_ARG): added to
  *            dW instead of replacing it.
  *   workspace  as above, of mpw_qlinear_grad_w_int8_workspace_bytes.

@@ -45,9 +45,9 @@ cudaError_t launch_expand_i8(const uint8_t* packed, int64_t N, int64_t K, int bi
 // Packed rows (4..15 bits) -> bf16_rn(s_n * q), rows of stride_bf16(K).
 cudaError_t launch_expand_bf16(const uint8_t* packed, const float* scales, int64_t N, int64_t K, int bits,
                                int layout, uint16_t* out, cudaStream_t stream);
-// 8-bit activations -> bf16 rows of stride_bf16(K): bf16_rn(sx * xq), and, with
-// parts == 3, in the M rows behind and the M behind those, what that leaves of
-// fl32(sx * xq), each rounded to bf16: together all of its 24 bits.
+// 8-bit activations -> bf16 rows of stride_bf16(K): bf16_rn(sx * xq), or, with
+// parts == 3, three blocks of M rows whose sum is fl32(sx * xq): its first 8
+// bits, the next 8 and the rest, all of its sign.
 cudaError_t launch_expand_x(const uint8_t* xq, const float* sx, int64_t M, int64_t K, int parts, uint16_t* out,
                             cudaStream_t stream);
 // bf16 [rows, cols] -> the same with rows of stride_bf16(cols).

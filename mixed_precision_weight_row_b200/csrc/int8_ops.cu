@@ -223,7 +223,31 @@ expand_bf16_kernel(const uint32_t* __restrict__ packed, const float* __restrict_
   }
 }
 
-// One thread per (token, 8 codes).
+// a as three bf16 values of its sign, all 24 bits of it (in steps of 2^-133, the
+// smallest bf16): the first 8 bits, the next 8, the rest.  Where a part would be
+// zero the part before it gives up its last step, so that none is (from 2^-124
+// on): the sum over the parts of an infinite dy times each must be an infinity,
+// not inf - inf or inf * 0.
+__device__ __forceinline__ void split3(float a, float (&part)[3]) {
+  uint32_t h = __float_as_uint(a) & 0xFFFF0000u;
+  float rest = a - __uint_as_float(h);
+  if (fabsf(rest) < 0x1p-132f && (h << 1) != 0u) {
+    h -= 0x10000u;
+    rest = a - __uint_as_float(h);
+  }
+  uint32_t m = __float_as_uint(rest) & 0xFFFF0000u;
+  float last = rest - __uint_as_float(m);
+  if (fabsf(last) < 0x1p-133f && (m << 1) != 0u) {
+    m -= 0x10000u;
+    last = rest - __uint_as_float(m);
+  }
+  part[0] = __uint_as_float(h);
+  part[1] = __uint_as_float(m);
+  part[2] = last;
+}
+
+// One thread per (token, 8 codes).  One part: sx xq rounded to bf16, what the
+// tensor cores multiply (off by at most 2^-8 of it, as the bf16 result once more).
 template <int PARTS>
 __global__ void __launch_bounds__(kThreads)
 expand_x_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ sx, int64_t M, int xstride, int stride,
@@ -242,14 +266,17 @@ expand_x_kernel(const uint8_t* __restrict__ xq, const float* __restrict__ sx, in
     for (int i = 0; i < 4; ++i) {
       const uint32_t u = i < 2 ? v.x : v.y;
       const int sh = 16 * (i & 1);
-      float a = s * static_cast<float>(static_cast<int8_t>(u >> sh));
-      float b = s * static_cast<float>(static_cast<int8_t>(u >> (sh + 8)));
+      float a[PARTS], b[PARTS];
+      a[0] = s * static_cast<float>(static_cast<int8_t>(u >> sh));
+      b[0] = s * static_cast<float>(static_cast<int8_t>(u >> (sh + 8)));
+      if constexpr (PARTS == 3) {
+        split3(a[0], a);
+        split3(b[0], b);
+      }
 #pragma unroll
       for (int p = 0; p < PARTS; ++p) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a[p], b[p]);
         part[p][i] = *reinterpret_cast<const uint32_t*>(&h);
-        a -= bf16_lo(part[p][i]);      // exact
-        b -= bf16_hi(part[p][i]);
       }
     }
 #pragma unroll

@@ -1,9 +1,10 @@
 """The int8 linear and the gradients at the ends of the number range and of
-their arguments: scales far from one."""
+their arguments: scales far from one, infinite gradients."""
 import numpy as np
 import pytest
 
 import oracle
+import workloads
 
 pytestmark = pytest.mark.gpu
 
@@ -39,6 +40,13 @@ def _inside(got, ref, bound, what):
     got = got.double().cpu().numpy()
     bad = ~(np.abs(got - ref) <= bound)
     assert not bad.any(), f"{what}: {bad.sum()} of {bad.size} out of bound, first at {np.argwhere(bad)[:3].tolist()}"
+
+
+def _same(got, want, what):
+    """Equal infinities and NaNs where the definition has them."""
+    got = got.double().cpu().numpy()
+    for f in (np.isnan, np.isposinf, np.isneginf):
+        assert np.array_equal(f(got), f(want)), what
 
 
 # ---- scales -----------------------------------------------------------------
@@ -92,3 +100,33 @@ def test_grad_x_largest_scales(mpw, b, M):
     dx = mpw.qlinear_grad_x(dy, packed, scales, b, K)
     ref, bound = oracle.grad_x_ref(dy.float().cpu().numpy(), q, s)
     _inside(dx, ref, bound, f"b={b} M={M}")
+
+
+# ---- infinite gradients -------------------------------------------------------
+
+
+@pytest.mark.parametrize("M,N,K", [(5, 40, 64), (16, 64, 128), (300, 130, 100), (1100, 257, 333), (4100, 300, 72)])
+@pytest.mark.parametrize("fp32", [False, True])
+def test_infinite_dy(mpw, M, N, K, fp32):
+    """inf times a nonzero code is an infinity, inf times a zero code NaN."""
+    torch = _torch()
+    x = workloads.gen_x(M, K, M)
+    x[1] = 0
+    x[2, :7] = torch.tensor([127.0, 64.0, -32.0, 1.0, -1.0, 3.0, 0.0])     # codes of a scale of 1: few bits each
+    x[2, 7:] = 5.0
+    x[3, ::3] = 0
+    xq, sx = mpw.quantize_x_int8(x.cuda())
+    dy = (torch.randn((M, N), generator=torch.Generator().manual_seed(1)) * 1e-3).to(torch.bfloat16)
+    clean = mpw.qlinear_grad_w_int8(dy.cuda(), xq, sx, K, dtype=torch.float32 if fp32 else torch.bfloat16)
+    inf = float("inf")
+    dy[2, 0], dy[3, 1], dy[M - 1, 2], dy[0, 4], dy[M - 1, 4] = inf, -inf, inf, inf, -inf
+    dy[1, 5] = inf
+    dW = mpw.qlinear_grad_w_int8(dy.cuda(), xq, sx, K, dtype=torch.float32 if fp32 else torch.bfloat16)
+    codes, sxr = oracle.quantize_x_int8(x.float().numpy())
+    xh = codes.astype(np.float64) * sxr.astype(np.float64)[:, None]
+    with np.errstate(invalid="ignore"):
+        want = (dy.double().numpy().T[:, :, None][:8] * xh[None]).sum(1)
+    _same(dW[:8], want, f"fp32={fp32} M={M} N={N} K={K}")
+    for n in (3, 6, 7):
+        assert torch.equal(dW[n], clean[n])
+    assert torch.equal(dW[8:], clean[8:])
