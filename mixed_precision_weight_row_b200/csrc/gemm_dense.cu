@@ -44,6 +44,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "int8_expand.cuh"
 #include "int8_internal.h"
 #include "lane_units.cuh"
 #include "mpw_internal.h"
@@ -114,7 +115,7 @@ __device__ __forceinline__ void bf16_pairs(const Args& p, int64_t c0, uint32_t (
       for (int c = 0; c < 32; ++c) {
         const float cs = __shfl_sync(0xffffffffu, mine, c);
         uint32_t& d = v[32 * h + c];
-        d = __float_as_uint(static_cast<float>(static_cast<int32_t>(d) >> p.shift) * cs * rs);
+        d = __float_as_uint(i8::scaled_sum(static_cast<int32_t>(d) >> p.shift, cs, rs));
       }
     }
   }

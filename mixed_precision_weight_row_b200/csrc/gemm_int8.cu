@@ -261,7 +261,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
           if (splits > 1) {
             reinterpret_cast<int32_t*>(fsmem)[t * BM + r] = static_cast<int32_t>(v[i]);
           } else if (m0 + t < M && n < N) {
-            const float o = static_cast<float>(static_cast<int32_t>(v[i]) >> (8 - B)) * sn * sx_s[t];
+            const float o = i8::scaled_sum(static_cast<int32_t>(v[i]) >> (8 - B), sn, sx_s[t]);
             y[static_cast<size_t>(m0 + t) * N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
           }
         }
@@ -294,7 +294,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
 #pragma unroll
         for (int i = 0; i < E; ++i)
           if (t0 + i < t1 && n < N) {
-            const float o = static_cast<float>(sum[i] >> (8 - B)) * sn * sx_s[t0 + i];
+            const float o = i8::scaled_sum(sum[i] >> (8 - B), sn, sx_s[t0 + i]);
             y[static_cast<size_t>(m0 + t0 + i) * N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
           }
       }

@@ -17,6 +17,16 @@
 namespace mpw {
 namespace i8 {
 
+// sum * s * t in fp32, the smaller scale first: a whole number times it is exact or
+// normal, and overflows only where the result does.  (In a fixed order rows of
+// large weights overflowed against small tokens.)  NaN stays NaN.
+__device__ __forceinline__ float scaled_sum(int32_t sum, float s, float t) {
+  float lo, hi;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(s), "f"(t));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(s), "f"(t));
+  return static_cast<float>(sum) * lo * hi;
+}
+
 // Byte mask of the left-justified field.
 template <int B>
 struct Just {

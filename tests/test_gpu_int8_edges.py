@@ -102,6 +102,27 @@ def test_grad_x_largest_scales(mpw, b, M):
     _inside(dx, ref, bound, f"b={b} M={M}")
 
 
+@pytest.mark.parametrize("M", [1, 2, 4, 40, 300, 1100])
+@pytest.mark.parametrize("b", [4, 6, 8])
+def test_qlinear_int8_scales_apart(mpw, b, M):
+    """Large weights with small tokens and the reverse: the result is finite
+    and normal, so no product on the way to it may overflow or lose bits."""
+    torch = _torch()
+    N, K = 40, 160
+    W = _w(N, K, 1)
+    q, _ = oracle.quantize(W, b)
+    packed, _ = _rows(mpw, W, b)
+    x = workloads.gen_x(M, K, 3)
+    codes, _ = oracle.quantize_x_int8(x.float().numpy())
+    xq, _ = mpw.quantize_x_int8(x.cuda())
+    for s_w, s_x in [(3e36, 1e-37), (4.8e37, 3e-40), (1e-38, 1e36), (2e-43, 1e36), (1e30, 1e-30), (1e-30, 1e30),
+                     (1e-20, 1e-19)]:
+        s, sx = np.full(N, s_w, np.float32), np.full(M, s_x, np.float32)
+        y = mpw.qlinear_int8(None, packed, torch.from_numpy(s).cuda(), b, xq=xq, sx=torch.from_numpy(sx).cuda(), K=K)
+        ref, bound = oracle.qlinear_int8_ref(codes, sx, q, s)
+        _inside(y, ref, bound, f"b={b} M={M} s={s_w} sx={s_x}")
+
+
 # ---- infinite gradients -------------------------------------------------------
 
 
