@@ -585,24 +585,28 @@ def qlinear_int8(x, packed, scales, bits: int, y=None, layout: str = "canonical"
                  workspace=None, stream=None):
     """Int8 linear for codes of 4..8 bits (mpw_qlinear_int8): quantizes x per
     token unless (xq, sx) are given (then x may be None and K names the number
-    of inputs), then y bf16 [M, N].  ``workspace``: uint8 of at least
-    qlinear_int8_workspace_bytes; allocated per call when None."""
+    of inputs; an x or K that disagrees is refused), then y bf16 [M, N].
+    ``workspace``: uint8 of at least qlinear_int8_workspace_bytes; allocated
+    per call when None."""
     torch = _torch()
-    dev = _here(packed, "packed")
-    bits = int(bits)
     if (xq is None) != (sx is None):
         raise ValueError("xq and sx go together")
+    if xq is not None and x is None and K is None:
+        raise ValueError("K is needed when only xq and sx are given")
+    dev = _here(packed, "packed")
+    bits = int(bits)
     if xq is None:
+        got = tuple(getattr(x, "shape", ()))
+        if K is not None and len(got) == 2 and got[1] != int(K):
+            raise ValueError(f"x must have shape (M, {int(K)}), got {got}")
         xq, sx = quantize_x_int8(x, stream=stream)
         M, K = x.shape
     else:
-        if K is None:
-            if x is None:
-                raise ValueError("K is needed when only xq and sx are given")
-            K = x.shape[1]
-        K = int(K)
+        K = int(x.shape[-1] if K is None else K)
         M = _arg(xq, "xq", torch.uint8, dev, (None, _row_bytes8(K)))
         _arg(sx, "sx", torch.float32, dev, (M,))
+        if x is not None and x.shape != (M, K):
+            raise ValueError(f"x must have shape {(M, K)}, got {tuple(x.shape)}")
     N = _rows_arg(packed, scales, bits, None, K, dev)
     lay = LAYOUTS[layout]
     handle = _stream(stream, dev)

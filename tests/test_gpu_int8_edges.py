@@ -1,5 +1,6 @@
 """The int8 linear and the gradients at the ends of the number range and of
-their arguments: scales far from one, infinite gradients."""
+their arguments: scales far from one, infinite gradients, contradictory
+arguments."""
 import numpy as np
 import pytest
 
@@ -151,3 +152,29 @@ def test_infinite_dy(mpw, M, N, K, fp32):
     for n in (3, 6, 7):
         assert torch.equal(dW[n], clean[n])
     assert torch.equal(dW[8:], clean[8:])
+
+
+# ---- arguments ------------------------------------------------------------------
+
+
+def test_contradictory_arguments_are_refused(mpw):
+    torch = _torch()
+    M, N, K = 20, 24, 64
+    packed, scales = _rows(mpw, _w(N, K, 1), 6)
+    x = workloads.gen_x(M, K, 1).cuda()
+    xq, sx = mpw.quantize_x_int8(x)
+    want = mpw.qlinear_int8(x, packed, scales, 6)
+    for kw in (dict(xq=xq, sx=sx), dict(xq=xq, sx=sx, K=K), dict(K=K)):
+        assert torch.equal(mpw.qlinear_int8(x, packed, scales, 6, **kw), want)
+    with pytest.raises(ValueError, match="xq and sx"):
+        mpw.qlinear_int8(None, packed, scales, 6, xq=xq)
+    with pytest.raises(ValueError, match="xq and sx"):
+        mpw.qlinear_int8(x, packed, scales, 6, sx=sx)
+    with pytest.raises(ValueError, match="K is needed"):
+        mpw.qlinear_int8(None, packed, scales, 6, xq=xq, sx=sx)
+    with pytest.raises(ValueError, match="x must have shape"):
+        mpw.qlinear_int8(x[1:], packed, scales, 6, xq=xq, sx=sx)
+    with pytest.raises(ValueError, match="x must have shape"):
+        mpw.qlinear_int8(x, packed, scales, 6, xq=xq, sx=sx, K=K - 1)
+    with pytest.raises(ValueError, match="x must have shape"):
+        mpw.qlinear_int8(x, packed, scales, 6, K=K - 1)

@@ -91,3 +91,14 @@ def test_binding_refuses_what_is_no_cuda_tensor():
         mpw.qlinear_grad_x(x, rows, s, 8, 16)
     with pytest.raises(ValueError):
         mpw.qlinear_grad_w_int8(x, rows, s, 16)
+
+
+def test_binding_refuses_incomplete_activations_before_anything_else():
+    x = torch.zeros((4, 16), dtype=torch.bfloat16)
+    rows = torch.zeros((4, 16), dtype=torch.uint8)
+    s = torch.ones(4)
+    for kw in (dict(xq=rows), dict(sx=s)):
+        with pytest.raises(ValueError, match="xq and sx"):
+            mpw.qlinear_int8(x, rows, s, 8, **kw)
+    with pytest.raises(ValueError, match="K is needed"):
+        mpw.qlinear_int8(None, rows, s, 8, xq=rows, sx=s)
