@@ -31,18 +31,27 @@ bool rows_are_bytes(int bits, int layout) { return bits == 8 && layout == MPW_LA
 // How a call of the int8 linear runs: a few tokens on the kernel that streams
 // packed rows, up to a thousand on the one that expands them on the way to the
 // tensor cores, more on expanded rows (the only one that takes a workspace).
-// One B200, us: 5120 x 6144, b = 6: 4 tokens 9.6 / 10.4 (first / second), 8
-// tokens 15.6 / 10.4; 5120 x 17408, b = 5: 2 tokens 14.7 / 19.5, 4 tokens 26.8
-// / 19.5; 17408 x 5120, b = 8: 4 tokens 20.1 / 17.3.  b = 6, second / third: 512
-// tokens 17408 x 5120 45 / 60, 5120 x 6144 22 / 26; 1024 tokens 86 / 84, 42 / 36,
-// 4096 x 4096 18 / 21; 1280 tokens 107 / 96, 43 / 36, 33 / 25.  Rows that already
-// are bytes need no expansion: 5120 x 6144, b = 8: 128 tokens 12.3 / 13.4, 256
-// tokens 16.2 / 13.8, 512 tokens 20.2 / 17.6.
+// One B200, us: 5120 x 6144, b = 6: 4 tokens 9.6 / 10.4 (first / second);
+// 5120 x 17408, b = 5: 2 tokens 14.7 / 19.5, 4 tokens 26.8 / 19.5; 17408 x 5120,
+// b = 8: 4 tokens 20.1 / 17.3.  b = 6, second / third: 512 tokens 17408 x 5120
+// 51 / 66, 5120 x 6144 22 / 26; 1024 tokens 93 / 85, 42 / 36, 4096 x 4096 18 / 21;
+// 1280 tokens 111 / 97, 44 / 37, 33 / 25.  Rows that already are bytes need no
+// expansion: 5120 x 6144, b = 8: 128 tokens 12.7 / 14.0, 256 tokens 16.6 / 14.1, 512
+// tokens 20.6 / 17.9.
+// The third kernel sums a tile's K in one place, so the second, which shares it
+// among four SMs, goes on where there are few tiles (256 tokens x 128 rows):
+// b = 6, 256 x 17408, 1025 tokens (10 tiles) 15.2 / 25.9, 4096 (32) 22.2 / 28.7, 8192
+// (64) 41.5 / 38.3; 512 x 5120, 2048 (32) 12.9 / 13.3, 4096 (64) 16.6 / 14.9; 128 x 4096,
+// 8192 (32) 11.6 / 10.9.  Bytes, if K is long enough to share: 256 x 17408, 193 tokens
+// (2 tiles) 10.6 / 25.4; 128 x 4096, 193 (1) 7.3 / 8.5; 512 x 5120, 1024 (16)
+// 9.9 / 10.7, 2048 (32) 11.3 / 10.7; but 512 x 2560, 193 (4) 8.1 / 7.2.
 enum class Int8Path { kGemv, kFused, kDense };
 Int8Path int8_path(int bits, int layout, int64_t M, int64_t N, int64_t K) {
   if ((M <= 2 || (M <= 4 && K <= 8192 && bits <= 7)) && gemv_i8_fits(bits, M, K)) return Int8Path::kGemv;
-  if (M <= (rows_are_bytes(bits, layout) ? 192 : 1024) && gemm_i8_fits(M, N)) return Int8Path::kFused;
-  return Int8Path::kDense;
+  if (!gemm_i8_fits(M, N)) return Int8Path::kDense;
+  const int64_t tiles = ((M + 255) / 256) * ((N + 127) / 128);
+  const bool fused = rows_are_bytes(bits, layout) ? M <= 192 || (K >= 4096 && tiles <= 16) : M <= 1024 || tiles <= 32;
+  return fused ? Int8Path::kFused : Int8Path::kDense;
 }
 
 // Room for the expanded rows of the int8 linear.

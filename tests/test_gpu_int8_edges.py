@@ -1,6 +1,6 @@
 """The int8 linear and the gradients at the ends of the number range and of
-their arguments: scales far from one, infinite gradients, contradictory
-arguments."""
+their arguments: scales far from one, many tokens through few rows, infinite
+gradients, contradictory arguments."""
 import numpy as np
 import pytest
 
@@ -122,6 +122,39 @@ def test_qlinear_int8_scales_apart(mpw, b, M):
         y = mpw.qlinear_int8(None, packed, torch.from_numpy(s).cuda(), b, xq=xq, sx=torch.from_numpy(sx).cuda(), K=K)
         ref, bound = oracle.qlinear_int8_ref(codes, sx, q, s)
         _inside(y, ref, bound, f"b={b} M={M} s={s_w} sx={s_x}")
+
+
+# ---- narrow outputs -------------------------------------------------------------
+
+
+@pytest.mark.parametrize("layout", ["canonical", "paired"])
+@pytest.mark.parametrize("N,K,M,b", [(40, 17408, 193, 8), (256, 2048, 700, 8), (256, 5120, 1025, 6), (130, 1024, 3001, 4),
+                                     (33, 96, 2000, 7), (1000, 512, 1030, 5), (16, 4096, 8192, 6), (16, 4096, 8193, 8)])
+def test_qlinear_int8_narrow_outputs(mpw, N, K, M, b, layout):
+    """Many tokens through few rows, on either side of the border between the
+    kernels: the exact sums."""
+    torch = _torch()
+    W = _w(N, K, N)
+    packed, scales = _rows(mpw, W, b, layout)
+    x = workloads.gen_x(M, K, M)
+    y = mpw.qlinear_int8(x.cuda(), packed, scales, b, layout=layout)
+    pick = np.unique(np.concatenate([[0, M - 1], np.random.default_rng(M).integers(0, M, 200)]))
+    q, s = oracle.quantize(W, b)
+    codes, sx = oracle.quantize_x_int8(x[torch.from_numpy(pick)].float().numpy())
+    ref, bound = oracle.qlinear_int8_ref(codes, sx, q, s)
+    _inside(y[torch.from_numpy(pick).cuda()], ref, bound, f"b={b} {layout} M={M} N={N} K={K}")
+    assert mpw.device_error() == 0
+
+
+def test_narrow_outputs_share_k(mpw):
+    """A product of few tiles runs where several SMs share a tile's K, which
+    takes no workspace for expanded rows, at any number of tokens that leaves
+    it few tiles; one of many tiles does not."""
+    f = mpw.lib.mpw_qlinear_int8_workspace_bytes
+    for M, N, K in [(1024, 256, 17408), (1025, 256, 17408), (4096, 256, 17408), (8192, 128, 17408), (2000, 512, 5120)]:
+        assert f(6, 0, M, N, K) == 0, (M, N, K)
+    for M, N, K in [(8193, 256, 17408), (1025, 17408, 5120), (1280, 4096, 4096)]:
+        assert f(6, 0, M, N, K) >= N * K, (M, N, K)
 
 
 # ---- infinite gradients -------------------------------------------------------
