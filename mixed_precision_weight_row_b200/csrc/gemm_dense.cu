@@ -111,12 +111,19 @@ __device__ __forceinline__ void bf16_pairs(const Args& p, int64_t c0, uint32_t (
 #pragma unroll
     for (int h = 0; h < C / 32; ++h) {
       const float mine = 32 * h + lane < left ? __ldg(p.col_scale + c0 + 32 * h + lane) : 0.0f;
+      auto scale = [&](auto of) {
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        const float cs = __shfl_sync(0xffffffffu, mine, c);
-        uint32_t& d = v[32 * h + c];
-        d = __float_as_uint(i8::scaled_sum(static_cast<int32_t>(d) >> p.shift, cs, rs));
-      }
+        for (int c = 0; c < 32; ++c) {
+          const float cs = __shfl_sync(0xffffffffu, mine, c);
+          uint32_t& d = v[32 * h + c];
+          d = __float_as_uint(of(static_cast<int32_t>(d) >> p.shift, cs));
+        }
+      };
+      // as a rule no column's scale is large (i8::RowScale)
+      if (__any_sync(0xffffffffu, mine > i8::RowScale::kLarge))
+        scale([&](int32_t sum, float cs) { return i8::RowScale(cs).of(sum, rs); });
+      else
+        scale([&](int32_t sum, float cs) { return static_cast<float>(sum) * cs * rs; });
     }
   }
 #pragma unroll

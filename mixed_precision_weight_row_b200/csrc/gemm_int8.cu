@@ -249,7 +249,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
     if (ok) {
       ptx::tc_fence_after();
       const int64_t n = n0 + r;
-      const float sn = n < N ? __ldg(scales + n) : 0.0f;
+      const i8::RowScale sn(n < N ? __ldg(scales + n) : 0.0f);
       constexpr int CH = BN < 32 ? BN : 32;        // tokens per step
       for (int c = wg; c < BN / CH; c += kGroups) {
         uint32_t v[32];
@@ -261,7 +261,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
           if (splits > 1) {
             reinterpret_cast<int32_t*>(fsmem)[t * BM + r] = static_cast<int32_t>(v[i]);
           } else if (m0 + t < M && n < N) {
-            const float o = i8::scaled_sum(static_cast<int32_t>(v[i]) >> (8 - B), sn, sx_s[t]);
+            const float o = sn.of(static_cast<int32_t>(v[i]) >> (8 - B), sx_s[t]);
             y[static_cast<size_t>(m0 + t) * N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
           }
         }
@@ -278,7 +278,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
       const int r = threadIdx.x & 127;
       const int64_t n = n0 + r;
       const int t1 = min(BN, M - m0);
-      const float sn = n < N ? __ldg(scales + n) : 0.0f;
+      const i8::RowScale sn(n < N ? __ldg(scales + n) : 0.0f);
       for (int t0 = E * (part * kGroups + ((warp - kConvWarp0) >> 2)); t0 < t1; t0 += E * splits * kGroups) {
         int32_t sum[E];
 #pragma unroll
@@ -294,7 +294,7 @@ gemm_i8_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant
 #pragma unroll
         for (int i = 0; i < E; ++i)
           if (t0 + i < t1 && n < N) {
-            const float o = i8::scaled_sum(sum[i] >> (8 - B), sn, sx_s[t0 + i]);
+            const float o = sn.of(sum[i] >> (8 - B), sx_s[t0 + i]);
             y[static_cast<size_t>(m0 + t0 + i) * N + n] = __bfloat16_as_ushort(__float2bfloat16_rn(o));
           }
       }

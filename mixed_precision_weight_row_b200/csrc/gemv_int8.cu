@@ -183,7 +183,7 @@ gemv_i8_kernel(const __grid_constant__ Args p, int32_t* err) {
       }
       if (lane < p.M && r0 + r < row1)
         p.y[static_cast<int64_t>(lane) * p.N + r0 + r] =
-            __bfloat16_as_ushort(__float2bfloat16_rn(i8::scaled_sum(sum >> (8 - B), sn[r], sx)));
+            __bfloat16_as_ushort(__float2bfloat16_rn(i8::RowScale(sn[r]).of(sum >> (8 - B), sx)));
     }
   }
 }

@@ -17,15 +17,17 @@
 namespace mpw {
 namespace i8 {
 
-// sum * s * t in fp32, the smaller scale first: a whole number times it is exact or
-// normal, and overflows only where the result does.  (In a fixed order rows of
-// large weights overflowed against small tokens.)  NaN stays NaN.
-__device__ __forceinline__ float scaled_sum(int32_t sum, float s, float t) {
-  float lo, hi;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(s), "f"(t));
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(s), "f"(t));
-  return static_cast<float>(sum) * lo * hi;
-}
+// A row's scale s for y = sum * s * sx in fp32: before sx, or after it if s is so
+// large that the sum (below 2^31) times it might overflow where y does not.  A whole
+// number times a scale loses nothing to underflow.
+struct RowScale {
+  float before, after;
+  static constexpr float kLarge = 0x1p64f;
+  explicit __device__ RowScale(float s) : before(s > kLarge ? 1.0f : s), after(s > kLarge ? s : 1.0f) {}
+  __device__ __forceinline__ float of(int32_t sum, float sx) const {
+    return static_cast<float>(sum) * before * sx * after;
+  }
+};
 
 // Byte mask of the left-justified field.
 template <int B>
