@@ -585,6 +585,9 @@ MPW_API mpw_status mpw_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, 
  *            need one each; it must live until the call has run (and, when
  *            captured, as long as the graph).  Missing or too small:
  *            MPW_E_INVALID_ARG.
+ *   y and the workspace share no byte with an input or with each other (else
+ *   MPW_E_INVALID_ARG; so for every call of this group, mpw_quantize_x_int8
+ *   and the gradients).
  *   Any M, N >= 1; 1 <= K <= 131071 (a 32-bit sum cannot overflow).
  *   One token or 2048, the result is the same exact sum, scaled in fp32 and
  *   rounded once.

@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "int8_internal.h"
 #include "mpw.h"
 #include "mpw_internal.h"
@@ -24,6 +26,24 @@ bool dims_ok(int64_t M, int64_t N, int64_t K) {
 // Result tiles are counted in 32 bits: up to 2^44 results, far beyond any memory.
 bool result_ok(int64_t I, int64_t J) { return I <= (int64_t{1} << 44) / J; }
 size_t round256(size_t b) { return (b + 255) & ~static_cast<size_t>(255); }
+
+// Memory of an argument, and whether `out` shares no byte with any of the others.
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool apart(const Span& out, std::initializer_list<Span> others) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(out.p);
+  for (const Span& o : others) {
+    const uintptr_t b = reinterpret_cast<uintptr_t>(o.p);
+    if (out.bytes != 0 && o.bytes != 0 && a < b + o.bytes && b < a + out.bytes) return false;
+  }
+  return true;
+}
+Span span(const void* p, int64_t rows, int64_t row_bytes) {
+  return {p, static_cast<size_t>(rows) * static_cast<size_t>(row_bytes)};
+}
+Span rows_span(const uint8_t* packed, int bits, int64_t N, int64_t K) { return span(packed, N, 4 * row_words(K, bits)); }
 
 // Canonical 8-bit rows already are rows of signed bytes.
 bool rows_are_bytes(int bits, int layout) { return bits == 8 && layout == MPW_LAYOUT_CANONICAL; }
@@ -86,6 +106,8 @@ extern "C" {
 mpw_status mpw_quantize_x_int8(const uint16_t* x, int64_t M, int64_t K, uint8_t* xq, float* sx, mpw_stream_t stream) {
   if (x == nullptr || xq == nullptr || sx == nullptr || !dims_ok(M, 1, K)) return MPW_E_INVALID_ARG;
   if (!aligned(x, 2) || !aligned(xq, 16) || !aligned(sx, 4)) return MPW_E_MISALIGNED;
+  const Span in = span(x, M, 2 * K), scales = span(sx, M, 4);
+  if (!apart(scales, {in}) || !apart(span(xq, M, stride_i8(K)), {in, scales})) return MPW_E_INVALID_ARG;
   return from_cuda(launch_quantize_x_int8(x, M, K, xq, sx, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -106,6 +128,10 @@ mpw_status mpw_qlinear_int8(const uint8_t* xq, const float* sx, const uint8_t* p
   const size_t need = mpw_qlinear_int8_workspace_bytes(bits, layout, M, N, K);
   if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return MPW_E_INVALID_ARG;
   if (need != 0 && !aligned(workspace, 16)) return MPW_E_MISALIGNED;
+  const Span in[4] = {span(xq, M, stride_i8(K)), span(sx, M, 4), rows_span(packed, bits, N, K), span(scales, N, 4)};
+  const Span scratch{workspace, need}, out = span(y, M, 2 * N);
+  if (!apart(out, {in[0], in[1], in[2], in[3], scratch}) || !apart(scratch, {in[0], in[1], in[2], in[3]}))
+    return MPW_E_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (int8_path(bits, layout, M, N, K)) {
     case Int8Path::kGemv: return from_cuda(launch_gemv_i8(xq, sx, packed, scales, bits, layout, M, N, K, y, s));
@@ -137,6 +163,9 @@ mpw_status mpw_qlinear_grad_x(const uint16_t* dy, const uint8_t* packed, const f
   const size_t need = mpw_qlinear_grad_x_workspace_bytes(bits, layout, M, N, K);
   if (need != 0 && (workspace == nullptr || workspace_bytes < need)) return MPW_E_INVALID_ARG;
   if (need != 0 && !aligned(workspace, 16)) return MPW_E_MISALIGNED;
+  const Span in[3] = {span(dy, M, 2 * N), rows_span(packed, bits, N, K), span(scales, N, 4)};
+  const Span scratch{workspace, need}, out = span(dx, M, 2 * K);
+  if (!apart(out, {in[0], in[1], in[2], scratch}) || !apart(scratch, {in[0], in[1], in[2]})) return MPW_E_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (gradx_fused(bits, M, N, K)) {
@@ -171,6 +200,9 @@ mpw_status mpw_qlinear_grad_w_int8(const uint16_t* dy, const uint8_t* xq, const 
   const size_t need = mpw_qlinear_grad_w_int8_workspace_bytes(dW_type, M, N, K);
   if (workspace == nullptr || workspace_bytes < need) return MPW_E_INVALID_ARG;
   if (!aligned(workspace, 16)) return MPW_E_MISALIGNED;
+  const Span in[3] = {span(dy, M, 2 * N), span(xq, M, stride_i8(K)), span(sx, M, 4)};
+  const Span scratch{workspace, need}, out = span(dW, N, (f32 ? 4 : 2) * K);
+  if (!apart(out, {in[0], in[1], in[2], scratch}) || !apart(scratch, {in[0], in[1], in[2]})) return MPW_E_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int parts = f32 ? 3 : 1;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

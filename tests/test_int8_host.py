@@ -102,3 +102,29 @@ def test_binding_refuses_incomplete_activations_before_anything_else():
             mpw.qlinear_int8(x, rows, s, 8, **kw)
     with pytest.raises(ValueError, match="K is needed"):
         mpw.qlinear_int8(None, rows, s, 8, xq=rows, sx=s)
+
+
+def test_overlapping_outputs_are_refused():
+    """An output, or the workspace, that shares bytes with an input or with one
+    another: blocks that finish early would overwrite what others still read."""
+    f = mpw.lib.mpw_quantize_x_int8                       # x 64 x 64 bf16: 8192 bytes, xq 4096, sx 256
+    for args in [(A, 64, 64, A, C), (A, 64, 64, A + 8176, C), (A + 4080, 64, 64, A, C), (A, 64, 64, B, A + 8188),
+                 (A, 64, 64, B, B + 4092), (A, 64, 64, B, B - 252)]:
+        assert f(*args, 0) == INV, args
+    # xq 64 x 64: 4096 bytes, sx 256, packed 32 x 48: 1536, scales 128, y 64 x 32 bf16: 4096
+    for kw in [dict(y=A), dict(y=A + 4094), dict(y=A - 4094), dict(y=B + 254), dict(y=C), dict(y=C + 1534), dict(y=D),
+               dict(y=D - 4094)]:
+        assert _lin(**kw) == INV, kw
+    need = mpw.lib.mpw_qlinear_int8_workspace_bytes(6, 0, 9000, 512, 64)
+    assert need == 512 * 64
+    big = dict(M=9000, N=512, xq=1 << 24, y=1 << 26, nb=need)
+    for kw in [dict(ws=C), dict(ws=1 << 24), dict(ws=(1 << 26) + 16), dict(ws=(1 << 26) - need + 16), dict(ws=D),
+               dict(ws=B)]:
+        assert _lin(**{**big, **kw}) == INV, kw
+    # dy 64 x 64 bf16: 8192 bytes, packed 64 x 48, scales 256, dx 64 x 64 bf16
+    for kw in [dict(dx=A), dict(dx=A + 8190), dict(dx=B + 3070), dict(dx=C), dict(dx=C - 8190)]:
+        assert _gx(**{**dict(N=64), **kw}) == INV, kw
+    # dy 64 x 32 bf16: 4096 bytes, xq 4096, sx 256, dW 32 x 64
+    for kw in [dict(dW=A + 4094), dict(dW=B), dict(dW=C + 254), dict(kind=1, dW=A - 8188), dict(dW=W), dict(ws=A),
+               dict(ws=B - 16), dict(ws=C)]:
+        assert _gw(**kw) == INV, kw
