@@ -54,8 +54,8 @@ bool rows_are_bytes(int bits, int layout) { return bits == 8 && layout == MPW_LA
 // One B200, us: 5120 x 6144, b = 6: 4 tokens 9.6 / 10.4 (first / second);
 // 5120 x 17408, b = 5: 2 tokens 14.7 / 19.5, 4 tokens 26.8 / 19.5; 17408 x 5120,
 // b = 8: 4 tokens 20.1 / 17.3.  b = 6, second / third: 512 tokens 17408 x 5120
-// 51 / 66, 5120 x 6144 22 / 26; 1024 tokens 93 / 85, 42 / 36, 4096 x 4096 18 / 21;
-// 1280 tokens 111 / 97, 44 / 37, 33 / 25.  Rows that already are bytes need no
+// 51 / 66, 5120 x 6144 22 / 26; 1024 tokens 93 / 85, 42 / 36, 4096 x 4096 18 / 21,
+// 1024 x 17408 22 / 30 (mixed there); 1280 tokens 111 / 97, 44 / 37, 33 / 25.  Rows that already are bytes need no
 // expansion: 5120 x 6144, b = 8: 128 tokens 12.7 / 14.0, 256 tokens 16.6 / 14.1, 512
 // tokens 20.6 / 17.9.
 // The third kernel sums a tile's K in one place, so the second, which shares it

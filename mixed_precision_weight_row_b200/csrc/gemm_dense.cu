@@ -14,8 +14,8 @@
 // result; one CTA per SM walks over the tiles.  Warp 0 of each fills a ring of
 // stages by TMA (128 bytes of r, or 64 steps of r, per stage and operand, in the
 // 128-byte swizzle), one thread of the first CTA issues the products for both
-// into one of two accumulators in tensor memory, and four warps of each write
-// the other one out meanwhile: bf16 rows of whole, aligned 16-byte units by TMA
+// into one of two accumulators in tensor memory, and eight warps of each (two per
+// 32 rows) write the other one out meanwhile: bf16 rows of whole, aligned 16-byte units by TMA
 // from a block of 32 rows x 128 bytes per warp in shared memory, others by the
 // lanes, which exchange values for coalesced stores in eight times the
 // instructions (grad_w of 64 x 17408 x 5120, which writes 178 MB: 37 us by TMA,
@@ -34,10 +34,11 @@
 // The fp32 result of grad_w is meant to hold fp32 accuracy.  Its operand x comes
 // as three bf16 values whose products are summed one after another, the
 // smallest first, and since tensor cores truncate a sum at every step (2048
-// tokens in one go were off by 1.3e-6 of the result, an fp32 product by 0.8e-6),
-// the sum runs over equal chunks of at most 768 tokens that the epilogue adds,
-// rounding to nearest, to the tile in memory (it stays in L2).  Off by 0.45e-6
-// with 1000 tokens, 0.6e-6 with 2048, 0.7e-6 with 8192.
+// tokens in one go are off by 2.1e-6 of the norm, 8192 by 9e-6, operands of one
+// sign by 5.6e-6 and 35e-6), the sum runs over equal chunks of at most 768 tokens
+// that the epilogue adds, rounding to nearest, to the tile in memory (it stays in
+// L2).  Off by 0.45e-6 with 1000 tokens, 0.6e-6 with 2048, 0.7e-6 with 8192;
+// operands of one sign 0.9e-6, 1.2e-6, 1.3e-6.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_bf16.h>

@@ -1,4 +1,4 @@
-// Int8 linear for tens to hundreds of tokens: packed rows expanded on the way
+// Int8 linear for tens to hundreds of tokens (more, where the rows are few): packed rows expanded on the way
 // to the tensor cores, y[m, n] = bf16(s_n sx_m sum_k xq[m, k] q[n, k]).
 //
 // DynaQuant, "Custom kernel architecture": packed codes are read from memory,

@@ -212,7 +212,8 @@ expand_bf16_kernel(const uint32_t* __restrict__ packed, const float* __restrict_
       dec::gemm_expand_group<B, PAIRED>(w, v);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        // the parts' sum is exact in fp32: the code has at most 15 bits
+        // the parts' sum is exact in fp32: the code has at most 15 bits (and the
+        // product rounded once, to the bf16 that the tensor cores multiply)
         const __nv_bfloat162 r = __floats2bfloat162_rn((bf16_lo(v[0][i]) + bf16_lo(v[1][i])) * s,
                                                        (bf16_hi(v[0][i]) + bf16_hi(v[1][i])) * s);
         o[i] = *reinterpret_cast<const uint32_t*>(&r);
